@@ -39,6 +39,9 @@ UNITS = [
     ("allocate", "allocate.cu", []),
     ("attention", "attention.cu", []),
     ("pack", "pack.cu", []),
+    ("text_cache", "text_cache.cu", []),
+    ("text_attention", "text_attention.cu", []),
+    ("text", "text.cu", []),
     ("tactkv", "tactkv.cu", []),
 ]
 

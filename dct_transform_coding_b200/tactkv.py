@@ -41,11 +41,17 @@ TACTKV_UNIFORM_ALLOC = 32
 TACTKV_ROTATE = 64
 TACTKV_HEAD_GAIN = 128
 
+TACTKV_TEXT_BF16 = 0
+TACTKV_TEXT_MXFP8 = 1
+TACTKV_TEXT_MXFP4 = 2
+TEXT_FORMATS = {"bf16": TACTKV_TEXT_BF16, "mxfp8": TACTKV_TEXT_MXFP8, "mxfp4": TACTKV_TEXT_MXFP4}
+
 HEADER_BYTES = 64
 EXPORTED = ("tactkv_payload_bytes", "tactkv_workspace_bytes", "tactkv_compress", "tactkv_decompress",
             "tactkv_compress_profiled", "tactkv_decompress_profiled", "tactkv_compress_noalloc",
             "tactkv_allocate", "tactkv_device_status", "tactkv_occupancy", "tactkv_max_batch",
             "tactkv_attention_workspace_bytes", "tactkv_attention_decode",
+            "tactkv_text_workspace_bytes", "tactkv_text_append", "tactkv_text_read", "tactkv_text_attention",
             "tactkv_status_string", "tactkv_lloyd_max_table", "tactkv_format_version", "tactkv_last_launches")
 
 
@@ -68,7 +74,19 @@ class tactkv_occupancy_t(ctypes.Structure):
                 ("shrink_vs_bf16", ctypes.c_double)]
 
 
+class tactkv_text_cache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class tactkv_text_batch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("row_starts", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 _P = ctypes.POINTER(tactkv_unit)
+_TC, _TB = ctypes.POINTER(tactkv_text_cache), ctypes.POINTER(tactkv_text_batch)
 _lib.tactkv_payload_bytes.restype = ctypes.c_size_t
 _lib.tactkv_payload_bytes.argtypes = [_P]
 _lib.tactkv_workspace_bytes.restype = ctypes.c_size_t
@@ -96,6 +114,19 @@ _lib.tactkv_attention_decode.restype = ctypes.c_int
 _lib.tactkv_attention_decode.argtypes = [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                          ctypes.c_void_p]
+_lib.tactkv_text_workspace_bytes.restype = ctypes.c_size_t
+_lib.tactkv_text_workspace_bytes.argtypes = [_TC] + [ctypes.c_int] * 5
+_lib.tactkv_text_append.restype = ctypes.c_int
+_lib.tactkv_text_append.argtypes = [_TC, _TB, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t,
+                                    ctypes.c_void_p]
+_lib.tactkv_text_read.restype = ctypes.c_int
+_lib.tactkv_text_read.argtypes = [_TC, _TB, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                  ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+_lib.tactkv_text_attention.restype = ctypes.c_int
+_lib.tactkv_text_attention.argtypes = [_TC, _TB, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_int64] + [ctypes.c_void_p] * 7 + [
+                                       ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
 _lib.tactkv_status_string.restype = ctypes.c_char_p
 _lib.tactkv_status_string.argtypes = [ctypes.c_int]
 _lib.tactkv_lloyd_max_table.restype = ctypes.c_int
@@ -377,4 +408,220 @@ def attention_decode(q: torch.Tensor, k_payload: torch.Tensor, v_payload: torch.
         ds = tactkv_device_status(workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
         if ds != TACTKV_OK:
             raise TactkvError(ds, "tactkv_attention_decode (device)")
+    return out, m, l
+
+
+# --------------------------------------------------------------------------------- text cache ---
+class TextCache:
+    """One layer's paged text K/V: the pools (uint8 tensors on one GPU) and their format.
+
+    fmt "bf16", "mxfp8" or "mxfp4".  k_pages, v_pages [n_pages, heads, page_tokens, head_dim * 16, 8 or 4 / 8] hold
+    the codes, k_scales, v_scales [n_pages, heads, page_tokens, head_dim / 32] the scale bytes (None
+    with "bf16", whose pools may also be bfloat16 tensors [..., head_dim]).  text_cache() allocates them."""
+
+    def __init__(self, fmt: str, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None):
+        self.format = TEXT_FORMATS[fmt]
+        if fmt == "bf16":
+            k_pages, v_pages = (x.view(torch.uint8) if x.dtype == torch.bfloat16 else x for x in (k_pages, v_pages))
+            k_scales = v_scales = None
+        pools = [k_pages, v_pages] + ([] if fmt == "bf16" else [k_scales, v_scales])
+        if any(x is None or x.dtype != torch.uint8 or not x.is_contiguous() or x.dim() != 4 or not x.is_cuda
+               or x.device != k_pages.device for x in pools):
+            raise ValueError("the text cache's pools are contiguous 4-D uint8 tensors on one GPU")
+        self.n_pages, self.heads, self.page_tokens, row_bytes = k_pages.shape
+        self.head_dim = row_bytes * 8 // (16, 8, 4)[self.format]
+        if v_pages.shape != k_pages.shape or any(x.shape != (*k_pages.shape[:3], self.head_dim // 32)
+                                                 for x in pools[2:]):
+            raise ValueError("the text cache's pools do not fit together")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self.device = k_pages.device
+        self.struct = tactkv_text_cache(self.format, self.heads, self.head_dim, self.page_tokens, self.n_pages,
+                                        *[x.data_ptr() for x in pools])
+        if tactkv_text_workspace_bytes(self, 0, 0, 0, 0, 0) == 0:
+            raise TactkvError(TACTKV_UNSUPPORTED_SHAPE, "TextCache")
+
+
+def text_cache(fmt: str, n_pages: int, heads: int, head_dim: int, *, page_tokens: int = 64, device="cuda") -> TextCache:
+    """A TextCache of zeroed pools."""
+    row = head_dim * (16, 8, 4)[TEXT_FORMATS[fmt]] // 8
+    shapes = [row, row] + ([] if fmt == "bf16" else [head_dim // 32] * 2)
+    return TextCache(fmt, *[torch.zeros((n_pages, heads, page_tokens, w), dtype=torch.uint8, device=device) for w in shapes])
+
+
+def tactkv_text_workspace_bytes(cache: TextCache, n_seqs: int, n_rows: int, q_heads: int, max_rows: int,
+                                max_kv_len: int) -> int:
+    return int(_lib.tactkv_text_workspace_bytes(cache.struct, n_seqs, n_rows, q_heads, max_rows, max_kv_len))
+
+
+def text_workspace(cache: TextCache, *, n_seqs: int, n_rows: int, max_rows: int = 1, q_heads: int = 0,
+                   max_kv_len: int = 0) -> torch.Tensor:
+    """Zeroed workspace for calls of up to these sizes (q_heads = 0: append and read alone)."""
+    nbytes = tactkv_text_workspace_bytes(cache, n_seqs, n_rows, q_heads, max_rows, max_kv_len)
+    if nbytes == 0:
+        raise TactkvError(TACTKV_INVALID_ARG, "text_workspace")
+    ws = torch.zeros(nbytes + 256, dtype=torch.uint8, device=cache.device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + nbytes]
+
+
+def text_tree(parents: Sequence[Sequence[int]], device="cuda") -> torch.Tensor:
+    """The tree words [rows] int64 of sequences whose drafted tokens hang under the given earlier ones:
+    parents[s][j] < j is the parent of sequence s's node j, -1 for a root.  Bit i of a node's word is set
+    for its ancestors and for itself."""
+    words = []
+    for seq in parents:
+        mine = []
+        for j, up in enumerate(seq):
+            if not -1 <= up < j or j >= 64:
+                raise ValueError("a node's parent is an earlier node of at most 64, or -1")
+            mine.append((mine[up] if up >= 0 else 0) | 1 << j)
+        words += [w - (1 << 64) if w >> 63 else w for w in mine]
+    return torch.tensor(words, dtype=torch.int64, device=device)
+
+
+def _text_batch(cache: TextCache, page_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
+                n_rows: int) -> tactkv_text_batch:
+    n_seqs, max_pages = page_table.shape
+    for x in (page_table, kv_lens, row_starts):
+        if x.dtype != torch.int32 or not x.is_contiguous() or x.device != cache.device:
+            raise ValueError("page_table, kv_lens and row_starts are contiguous int32 tensors on the cache's GPU")
+    if kv_lens.numel() != n_seqs or row_starts.numel() != n_seqs + 1:
+        raise ValueError("page_table [n_seqs, max_pages], kv_lens [n_seqs], row_starts [n_seqs + 1]")
+    return tactkv_text_batch(page_table.data_ptr(), kv_lens.data_ptr(), row_starts.data_ptr(), n_seqs, n_rows, max_pages)
+
+
+class _text_call:
+    """The device and stream of one call: what the wrapper allocates and converts belongs to that stream."""
+
+    def __init__(self, cache: TextCache, stream: Optional[torch.cuda.Stream]):
+        self.ctx = None
+        if stream is not None:
+            if stream.device != cache.device:
+                raise ValueError("the stream is not on the cache's GPU")
+            self.ctx = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != cache.device.index:
+            self.ctx = torch.cuda.device(cache.device)
+        self.device = cache.device
+
+    def __enter__(self) -> int:
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _text_done(status: int, what: str, check: bool, workspace: torch.Tensor, stream_ptr: int) -> None:
+    if status != TACTKV_OK:
+        raise TactkvError(status, what)
+    if check:
+        ds = tactkv_device_status(workspace.data_ptr(), workspace.numel(), stream_ptr)
+        if ds != TACTKV_OK:
+            raise TactkvError(ds, what + " (device)")
+
+
+_TEXT_IO = {torch.bfloat16: 0, torch.float32: TACTKV_FP32_IO}
+
+
+def _text_pair(cache: TextCache, k: torch.Tensor, v: torch.Tensor, write: bool):
+    """k and v [rows, heads, head_dim] with one pair of strides, as the library takes them."""
+    if (k.dtype not in _TEXT_IO or v.dtype != k.dtype or k.dim() != 3 or v.shape != k.shape
+            or k.shape[1:] != (cache.heads, cache.head_dim) or k.device != cache.device or v.device != cache.device):
+        raise ValueError("k and v [rows, heads, head_dim] are bfloat16 or float32 tensors on the cache's GPU")
+    if k.stride() != v.stride() or k.stride(2) != 1 or k.stride(0) <= 0:
+        if write:
+            raise ValueError("k and v have equal strides, and neighbouring values along head_dim")
+        k, v = k.contiguous(), v.contiguous()
+    return k, v
+
+
+def text_append(cache: TextCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                row_starts: torch.Tensor, *, values: bool = False, workspace: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None, check: bool = False):
+    """Write k, v [rows, heads, head_dim] (bfloat16 or float32) into the cache: the rows row_starts[s] ..
+    row_starts[s+1] are sequence s's newest tokens, at positions kv_lens[s] - n .. kv_lens[s] - 1 (kv_lens counts
+    them).  page_table [n_seqs, max_pages], kv_lens and row_starts are int32 on the GPU.  With values, returns
+    (k, v) as the cache now holds them (rows behind the last sequence are left unset)."""
+    with _text_call(cache, stream) as stream_ptr:
+        k, v = _text_pair(cache, k, v, False)
+        batch = _text_batch(cache, page_table, kv_lens, row_starts, k.shape[0])
+        out = (torch.empty(k.shape, dtype=k.dtype, device=k.device), torch.empty(k.shape, dtype=k.dtype, device=k.device)) if values else None
+        if workspace is None:
+            workspace = text_workspace(cache, n_seqs=0, n_rows=0)
+        st = _lib.tactkv_text_append(cache.struct, batch, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                                     out[0].data_ptr() if values else None, out[1].data_ptr() if values else None,
+                                     _TEXT_IO[k.dtype], workspace.data_ptr(), workspace.numel(), stream_ptr)
+        _text_done(st, "tactkv_text_append", check, workspace, stream_ptr)
+    return out
+
+
+def text_read(cache: TextCache, page_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor, *,
+              n_rows: int, dtype=torch.bfloat16, out=None, workspace: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None, check: bool = False):
+    """Read the newest row_starts[s+1] - row_starts[s] tokens of every sequence (all kv_lens[s] of them, if that is
+    as many): (k, v) [n_rows, heads, head_dim], into the pair out if given (rows behind the last sequence are
+    left as they are)."""
+    with _text_call(cache, stream) as stream_ptr:
+        if out is None:
+            shape = (n_rows, cache.heads, cache.head_dim)
+            out = (torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device))
+        k, v = _text_pair(cache, *out, True)
+        if k.shape[0] != n_rows:
+            raise ValueError("out holds n_rows rows")
+        batch = _text_batch(cache, page_table, kv_lens, row_starts, n_rows)
+        if workspace is None:
+            workspace = text_workspace(cache, n_seqs=0, n_rows=0)
+        st = _lib.tactkv_text_read(cache.struct, batch, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                                   _TEXT_IO[k.dtype], workspace.data_ptr(), workspace.numel(), stream_ptr)
+        _text_done(st, "tactkv_text_read", check, workspace, stream_ptr)
+    return out
+
+
+def text_attention(q: torch.Tensor, cache: TextCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                   row_starts: torch.Tensor, *, max_rows: int, max_kv_len: Optional[int] = None,
+                   tree: Optional[torch.Tensor] = None, prior=None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                   check: bool = False):
+    """Attention of the newest rows q [rows, q_heads, head_dim] (bfloat16 or float32) over their sequences' cached
+    tokens, those rows' own among them: one generated token for each sequence (max_rows = 1), or up to 64
+    drafted ones whose tree words (text_tree) say which of the others each sees (None: the ones before it).
+    max_kv_len bounds kv_lens (default: what the page table holds).  prior = (out, m, l) merges the same
+    queries' attention over other tokens, as attention_decode returns it (float32).  Returns (out, m, l): out
+    like q; m and l float32 [rows, q_heads], the scores' maximum and exp-sum with the prior's.  Rows behind the last
+    sequence are left as they are."""
+    with _text_call(cache, stream) as stream_ptr:
+        if q.dtype not in _TEXT_IO or q.dim() != 3 or q.shape[2] != cache.head_dim or q.device != cache.device:
+            raise ValueError("q [rows, q_heads, head_dim] is a bfloat16 or float32 tensor on the cache's GPU")
+        n_rows, q_heads, D = q.shape
+        if q.stride(2) != 1 or q.stride(0) % 8 or q.stride(1) % 8 or q.data_ptr() % 16:
+            q = q.clone(memory_format=torch.contiguous_format)
+        if out is None:
+            out = torch.empty((n_rows, q_heads, D), dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
+            raise ValueError("out is a contiguous tensor of q's shape, type and device")
+        ml = torch.empty((2, n_rows, q_heads), dtype=torch.float32, device=q.device)
+        if tree is not None and (tree.dtype != torch.int64 or tree.numel() != n_rows or not tree.is_contiguous()
+                                 or tree.device != q.device):
+            raise ValueError("tree holds an int64 word for each row")
+        ptrs = (None, None, None)
+        if prior is not None:
+            for x, shape in zip(prior, ((n_rows, q_heads, D), (n_rows, q_heads), (n_rows, q_heads))):
+                if x.shape != shape or x.dtype != torch.float32 or not x.is_contiguous() or x.device != q.device:
+                    raise ValueError("prior = (out, m, l): contiguous float32 [rows, q_heads, head_dim], [rows, q_heads] (twice)")
+            ptrs = tuple(x.data_ptr() for x in prior)
+        batch = _text_batch(cache, page_table, kv_lens, row_starts, n_rows)
+        if max_kv_len is None:
+            max_kv_len = min(page_table.shape[1] * cache.page_tokens, 2 ** 31 - 1)
+        if workspace is None:
+            workspace = text_workspace(cache, n_seqs=batch.n_seqs, n_rows=n_rows, max_rows=max_rows, q_heads=q_heads,
+                                       max_kv_len=max_kv_len)
+        m, l = ml
+        st = _lib.tactkv_text_attention(cache.struct, batch, q_heads, max_rows, max_kv_len, q.data_ptr(), q.stride(0),
+                                        q.stride(1), None if tree is None else tree.data_ptr(), *ptrs, out.data_ptr(),
+                                        m.data_ptr(), l.data_ptr(), _TEXT_IO[q.dtype], workspace.data_ptr(),
+                                        workspace.numel(), stream_ptr)
+        _text_done(st, "tactkv_text_attention", check, workspace, stream_ptr)
     return out, m, l

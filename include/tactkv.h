@@ -213,6 +213,118 @@ tactkv_status tactkv_attention_decode(const tactkv_unit* k_units, const tactkv_u
                                       void* workspace, size_t workspace_bytes,
                                       struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------------------------------
+   Text K/V.  The codec compresses the visual K/V of a finished prefill; the text K/V of the same
+   layer grows by the tokens that a decode step adds.  The three calls below keep it in a paged cache
+   (as bfloat16, or quantized as it is written), read it back, and attend to it, merging the
+   (out, m, l) partial that tactkv_attention_decode returns for the visual tokens.
+
+   Formats.  A token's head_dim values in one K/V head are held as
+     TACTKV_TEXT_BF16   bfloat16 (float32 input is rounded to nearest even);
+     TACTKV_TEXT_MXFP8  E4M3 codes, one byte each;
+     TACTKV_TEXT_MXFP4  E2M1 codes, two to a byte, the even index in the low half;
+   the coded formats with one E8M0 scale byte s for each 32 values: a code c stands for
+   c * 2^(s - 127).  s is the smallest byte that brings the group's largest magnitude within the
+   code's largest value (448; 6), so scaling by it is exact and the one rounding is that to the code's
+   grid, to nearest even; no value is clipped.  A group that holds an infinity or a NaN gets s = 255
+   and reads back as NaN throughout.
+
+   Pages.  k_pages and v_pages hold n_pages pages of page_tokens tokens:
+     code byte i of (page, head, token) at ((page*heads + head)*page_tokens + token)*row_bytes + i,
+     row_bytes = head_dim * 16, 8 or 4 / 8;
+     scale j at ((page*heads + head)*page_tokens + token)*(head_dim/32) + j of k_scales / v_scales
+     (not used with TACTKV_TEXT_BF16).
+   heads >= 1, head_dim a multiple of 32 up to 256, page_tokens a power of two, 16 to 1024; every
+   pool 16-byte aligned.
+
+   Rows.  A call works on n_rows rows of activations: sequence s owns rows row_starts[s] ..
+   row_starts[s+1]-1 (row_starts[0] = 0, not decreasing), n_s of them, which stand for the cache positions
+   kv_lens[s] - n_s .. kv_lens[s] - 1: kv_lens counts the sequence's tokens with these rows among
+   them.  Position t is token t % page_tokens of page page_table[s*max_pages + t / page_tokens].  Rows
+   from row_starts[n_seqs] on (a padded batch) are neither read nor written.  page_table, kv_lens and
+   row_starts are DEVICE arrays of int32, read when the kernels run, so that a captured call can be
+   replayed on other lengths and pages.  A page may be shared by sequences that only read it; a
+   position that a call appends to must belong to one sequence alone.
+
+   Errors found by the kernels are recorded as TACTKV_INVALID_ARG in the workspace (zeroed by the
+   caller before its first use; tactkv_device_status): rows, lengths or tables that do not fit together
+   (n_s < 0, kv_lens[s] < n_s, more tokens than max_pages pages hold or, for attention, than
+   max_kv_len, more rows than n_rows or max_rows) and page numbers outside 0 .. n_pages-1.  Nothing is
+   read or written outside the arrays: append skips such rows, read zero-fills them, and attention
+   leaves the tokens of such pages, or all tokens of such a sequence, out. */
+#define TACTKV_TEXT_BF16  0
+#define TACTKV_TEXT_MXFP8 1
+#define TACTKV_TEXT_MXFP4 2
+
+typedef struct {
+  int32_t format;             /* TACTKV_TEXT_* */
+  int32_t heads, head_dim;    /* K/V heads */
+  int32_t page_tokens;
+  int64_t n_pages;            /* pages in each pool */
+  void* k_pages;
+  void* v_pages;
+  void* k_scales;             /* NULL with TACTKV_TEXT_BF16 */
+  void* v_scales;
+} tactkv_text_cache;
+
+typedef struct {
+  const int32_t* page_table;  /* DEVICE [n_seqs][max_pages] */
+  const int32_t* kv_lens;     /* DEVICE [n_seqs] */
+  const int32_t* row_starts;  /* DEVICE [n_seqs + 1] */
+  int32_t n_seqs, n_rows, max_pages;
+} tactkv_text_batch;
+
+/* Workspace of the three calls: a status word for append and read (q_heads = 0), and for attention
+   the partial results of the parts that long sequences are split into.  0 if the cache or the numbers
+   are not supported. */
+size_t tactkv_text_workspace_bytes(const tactkv_text_cache* cache, int n_seqs, int n_rows, int q_heads,
+                                   int max_rows, int max_kv_len);
+
+/* Write the rows' K and V into the cache.  Element (row, head, d) is at k + row*token_stride +
+   head*head_stride + d (v alike; elements): bfloat16, or float32 with TACTKV_FP32_IO in flags (the only
+   flag).  Strides even, k and v 4-byte aligned (8-byte with TACTKV_FP32_IO).  k_values, v_values: NULL
+   or DEVICE [n_rows][heads][head_dim] of the same type, 16-byte aligned, which receive the values that the
+   cache now holds, rounded to that type.  Asynchronous on `stream`; one kernel. */
+tactkv_status tactkv_text_append(const tactkv_text_cache* cache, const tactkv_text_batch* batch, const void* k,
+                                 const void* v, int64_t token_stride, int64_t head_stride, void* k_values,
+                                 void* v_values, uint32_t flags, void* workspace, size_t workspace_bytes,
+                                 struct CUstream_st* stream);
+
+/* Read the rows' K and V from the cache into k and v (indexed and typed as for append).  With n_s =
+   kv_lens[s] that is the whole sequence.  Asynchronous on `stream`; one kernel. */
+tactkv_status tactkv_text_read(const tactkv_text_cache* cache, const tactkv_text_batch* batch, void* k, void* v,
+                               int64_t token_stride, int64_t head_stride, uint32_t flags, void* workspace,
+                               size_t workspace_bytes, struct CUstream_st* stream);
+
+/* Attention of the rows over their sequences' cached tokens: the rows are the last generated token
+   (n_s = 1) or a tree of drafted tokens, appended before this call.
+     q_heads     query heads, a multiple G of the cache's heads (G <= 16); query head j reads K/V head j/G;
+     max_rows    a bound on every n_s, 1 to 64; max_kv_len a bound on every kv_lens[s] (both size the launch
+                 and the workspace);
+     q           (row, head, d) at q + row*q_token_stride + head*q_head_stride + d: bfloat16, or float32
+                 with TACTKV_FP32_IO; 16-byte aligned, strides multiples of 8 elements;
+     tree        NULL or DEVICE [n_rows]: bit j of row i's word lets it see row j of its own sequence
+                 (its ancestors and itself, for a tree).  NULL: rows 0 .. i.  Every row sees all
+                 kv_lens[s] - n_s tokens before the rows;
+     prior_out, prior_m, prior_l
+                 all NULL, or DEVICE float32 [n_rows][q_heads][head_dim], [n_rows][q_heads] (twice): the
+                 attention of the same queries over other tokens, as tactkv_attention_decode returns it,
+                 to be merged;
+     out         [n_rows][q_heads][head_dim], bfloat16 or float32 like q: softmax(q K^T / sqrt(head_dim)) V
+                 over the tokens seen (and the prior's), 16-byte aligned;
+     m, l        float32 [n_rows][q_heads]: the scores' maximum and sum_t exp(score - m).
+   A row that sees nothing gets out = 0, m = -inf, l = 0.  Values at positions that a row does not see
+   do not reach it, be they infinities or NaN.  Scores and sums are float32; with bfloat16 q the
+   probabilities are rounded to 11 or 8 bits before they multiply V, with float32 q they are not.
+   workspace: tactkv_text_workspace_bytes() with the same numbers, 256-byte aligned; calls that may
+   overlap need workspaces of their own.  Asynchronous on `stream`. */
+tactkv_status tactkv_text_attention(const tactkv_text_cache* cache, const tactkv_text_batch* batch, int q_heads,
+                                    int max_rows, int max_kv_len, const void* q, int64_t q_token_stride,
+                                    int64_t q_head_stride, const uint64_t* tree, const float* prior_out,
+                                    const float* prior_m, const float* prior_l, void* out, float* m, float* l,
+                                    uint32_t flags, void* workspace, size_t workspace_bytes,
+                                    struct CUstream_st* stream);
+
 /* Synchronizes `stream`, returns the first error the kernels recorded in `workspace` since the
    previous call (TACTKV_OK if none), and clears it. */
 tactkv_status tactkv_device_status(void* workspace, size_t workspace_bytes,
