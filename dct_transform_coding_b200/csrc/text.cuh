@@ -3,7 +3,6 @@
 #pragma once
 
 #include <cuda_fp8.h>
-#include <cuda_fp4.h>
 
 #include "common.cuh"
 
@@ -95,16 +94,28 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
-__device__ __forceinline__ uint32_t pack_e2m1x2(float a, float b) {
-  return __nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest);
+// Eight E2M1 codes, the first in the lowest half byte, to nearest even.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8]) {
+  uint32_t w;
+  asm("{\n.reg .b8 a, b, c, d;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\ncvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\ncvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      "mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(w)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return w;
 }
-// Two E4M3 codes (16 bits), or two E2M1 codes (8 bits), as float32.
+// Eight E2M1 codes as four pairs of half-precision values (exact).
+__device__ __forceinline__ void unpack_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\ncvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\ncvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Two E4M3 codes (16 bits) as float32.
 __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-__device__ __forceinline__ float2 unpack_e2m1x2(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)v, __NV_E2M1);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
@@ -119,12 +130,14 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
 template <int FMT>
 __device__ __forceinline__ void decode8(const uint32_t (&w)[4], uint32_t scale, float (&x)[8]) {
   const float f = FMT == kBf16 ? 1.f : scale_value(scale);
+  uint32_t h[4];
+  if constexpr (FMT == kFp4) unpack_e2m1x8(w[0], h);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 v;
     if constexpr (FMT == kBf16) v = unpack_bf16x2(w[i]);
     else if constexpr (FMT == kFp8) v = unpack_e4m3x2(w[i / 2] >> (16 * (i & 1)) & 0xFFFFu);
-    else v = unpack_e2m1x2(w[0] >> (8 * i) & 0xFFu);
+    else v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
     x[2 * i] = FMT == kBf16 ? v.x : v.x * f;
     x[2 * i + 1] = FMT == kBf16 ? v.y : v.y * f;
   }

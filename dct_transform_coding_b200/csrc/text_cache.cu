@@ -155,8 +155,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Cache c, const B
         w[0] = pack_e4m3x4(u[0], u[1], u[2], u[3]);
         w[1] = pack_e4m3x4(u[4], u[5], u[6], u[7]);
       } else {
-        w[0] = pack_e2m1x2(u[0], u[1]) | pack_e2m1x2(u[2], u[3]) << 8 | pack_e2m1x2(u[4], u[5]) << 16 |
-               pack_e2m1x2(u[6], u[7]) << 24;
+        // The shuffle (of a lane's own word) keeps the compiler from folding the unpacking of the values
+        // below into this packing: nvcc 12.9 then loses the word's upper bytes.
+        w[0] = __shfl_sync(~0u, pack_e2m1x8(u), threadIdx.x & 31);
       }
       if (mine && (threadIdx.x & 3) == 0) c.scales[kv][at * (c.head_dim / kGroup) + d / kGroup] = (unsigned char)s;
     }
