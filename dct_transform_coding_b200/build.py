@@ -40,7 +40,8 @@ UNITS = [
     ("attention", "attention.cu", []),
     ("pack", "pack.cu", []),
     ("text_cache", "text_cache.cu", []),
-    ("text_attention", "text_attention.cu", []),
+    *[(f"text_attention_{d}", "text_attention.cu", [f"-DTACTKV_TEXT_D={d}"]) for d in range(32, 257, 32)],
+    ("text_parts", "text_parts.cu", []),
     ("text", "text.cu", []),
     ("tactkv", "tactkv.cu", []),
 ]

@@ -79,7 +79,7 @@ size_t tactkv_text_workspace_bytes(const tactkv_text_cache* cache, int n_seqs, i
   Cache c;
   if (check_cache(cache, c) != TACTKV_OK || n_seqs < 0 || n_rows < 0 || q_heads < 0 || max_rows < 0 || max_kv_len < 0)
     return 0;
-  return kStatusBytes;
+  return kStatusBytes + (q_heads ? attention_workspace(c.head_dim) : 0);
 }
 
 tactkv_status tactkv_text_append(const tactkv_text_cache* cache, const tactkv_text_batch* batch, const void* k,
@@ -125,7 +125,7 @@ tactkv_status tactkv_text_attention(const tactkv_text_cache* cache, const tactkv
   tactkv_status st = check(cache, batch, flags, a.c, a.b);
   if (st != TACTKV_OK) return st;
   if (q_heads < 1 || max_rows < 1 || max_kv_len < 0) return TACTKV_INVALID_ARG;
-  if (max_rows > kMaxRows || q_heads % a.c.heads || q_heads / a.c.heads > kMaxGroup) return TACTKV_UNSUPPORTED_SHAPE;
+  if (max_rows > kMaxRows || max_kv_len > kMaxLen || a.b.n_seqs > 65535 || q_heads % a.c.heads || q_heads / a.c.heads > kMaxGroup) return TACTKV_UNSUPPORTED_SHAPE;
   st = check_workspace(workspace, workspace_bytes,
                        tactkv_text_workspace_bytes(cache, a.b.n_seqs, a.b.n_rows, q_heads, max_rows, max_kv_len));
   if (st != TACTKV_OK || !a.b.n_seqs || !a.b.n_rows) return st;
@@ -133,7 +133,7 @@ tactkv_status tactkv_text_attention(const tactkv_text_cache* cache, const tactkv
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(m, 4) || !aligned(l, 4) || !aligned(tree, 8) ||
       !aligned(prior_out, 16) || !aligned(prior_m, 4) || !aligned(prior_l, 4) || q_token_stride % 8 || q_head_stride % 8)
     return TACTKV_ALIGNMENT;
-  if (too_many(a.b, q_heads)) return TACTKV_UNSUPPORTED_SHAPE;
+  if (too_many(a.b, q_heads) || a.c.heads > 65535 / kMaxRows) return TACTKV_UNSUPPORTED_SHAPE;
   a.q_heads = q_heads;
   a.max_rows = max_rows;
   a.max_len = max_kv_len;
@@ -148,7 +148,8 @@ tactkv_status tactkv_text_attention(const tactkv_text_cache* cache, const tactkv
   a.m = m;
   a.l = l;
   a.status = static_cast<unsigned int*>(workspace);
-  return launch_attention(cache->format, flags & TACTKV_FP32_IO, a, stream) == cudaSuccess ? TACTKV_OK : TACTKV_CUDA;
+  return launch_attention(cache->format, flags & TACTKV_FP32_IO, a, static_cast<unsigned char*>(workspace) + kStatusBytes,
+                          stream) == cudaSuccess ? TACTKV_OK : TACTKV_CUDA;
 }
 
 }  // extern "C"

@@ -12,6 +12,7 @@ namespace text {
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxRows = 64;          // rows of one sequence in an attention call: a tree word's bits
 constexpr int kMaxGroup = 16;         // query heads per K/V head
+constexpr int kMaxLen = 1 << 30;      // tokens of one sequence in an attention call
 constexpr int kGroup = 32;            // values that share a scale
 
 enum Format { kBf16 = TACTKV_TEXT_BF16, kFp8 = TACTKV_TEXT_MXFP8, kFp4 = TACTKV_TEXT_MXFP4 };
@@ -161,7 +162,8 @@ struct AttnArgs {
   float *m, *l;
   unsigned int* status;
 };
-cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, cudaStream_t st);
+size_t attention_workspace(int head_dim);   // bytes behind the status word
+cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspace, cudaStream_t st);
 
 }  // namespace text
 }  // namespace tactkv

@@ -1,0 +1,88 @@
+// Attention over the text cache: the launch plan, and the sum over a sequence's parts.
+#include "text_attention.cuh"
+
+namespace tactkv {
+namespace text {
+
+#define TACTKV_FOR_D(X) X(32) X(64) X(96) X(128) X(160) X(192) X(224) X(256)
+#define TACTKV_DECL(D) cudaError_t launch_parts_##D(int, bool, const AttnArgs&, const Parts&, cudaStream_t);
+TACTKV_FOR_D(TACTKV_DECL)
+#undef TACTKV_DECL
+
+namespace {
+
+constexpr int kThreads = 128;
+
+// out, m and l of one (row, query head): its parts' sums, each to the largest maximum, in the parts' order.
+template <bool F32>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, const Parts p, int tiles) {
+  __shared__ float4 sum[kThreads];
+  __shared__ float part_l[kThreads];
+  const int D = a.c.head_dim, G = a.q_heads / a.c.heads;
+  const int unit = blockIdx.y, tile = unit % tiles, head = unit / tiles % a.c.heads, seq = unit / tiles / a.c.heads;
+  const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
+  const int row = tile * kTileRows + blockIdx.x;
+  if (!sp.ok || row >= sp.rows * G) return;
+  const int n = max(1, (sp.len + p.tokens - 1) / p.tokens);
+  const long long stride = (long long)gridDim.y * kTileRows, at = (long long)unit * kTileRows + blockIdx.x;
+  const int cols = D / 4, groups = kThreads / cols, g = threadIdx.x / cols, d = threadIdx.x % cols * 4;
+  float m = -INFINITY;
+  for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, p.ml[i * stride + at].x);
+#pragma unroll
+  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+  const float safe = m == -INFINITY ? 0.f : m;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  if (g < groups) {
+#pragma unroll 4
+    for (int i = g; i < n; i += groups) {
+      const float2 ml = p.ml[i * stride + at];
+      const float4 x = *reinterpret_cast<const float4*>(p.o + (i * stride + at) * D + d);
+      const float f = exp2f(ml.x - safe);
+      l += ml.y * f;
+      v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+    }
+  }
+  sum[threadIdx.x] = v;
+  part_l[threadIdx.x] = l;
+  __syncthreads();
+  if (g) return;
+  for (int i = 1; i < groups; ++i) {
+    const float4 x = sum[i * cols + threadIdx.x];
+    l += part_l[i * cols + threadIdx.x];
+    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  }
+  finish4<F32>(a, (long long)(sp.first + row / G) * a.q_heads + head * G + row % G, d, v, m, l);
+}
+
+}  // namespace
+
+size_t attention_workspace(int head_dim) {
+  return (size_t)kMaxParts * kTileRows * (head_dim * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspace, cudaStream_t st) {
+  const int tiles = (a.max_rows * (a.q_heads / a.c.heads) + kTileRows - 1) / kTileRows;
+  const long long units = (long long)a.b.n_seqs * a.c.heads * tiles;
+  Parts p;
+  const long long most = (a.max_len + kLeastPart - 1) / kLeastPart;
+  p.count = (int)std::max(1ll, std::min(most, kMaxParts / units));
+  p.tokens = std::max(kLeastPart, ((a.max_len + p.count - 1) / p.count + 63) / 64 * 64);
+  p.count = std::max(1, (a.max_len + p.tokens - 1) / p.tokens);
+  p.o = static_cast<float*>(workspace);
+  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kMaxParts * kTileRows * a.c.head_dim);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (a.c.head_dim) {
+#define TACTKV_CASE(D) case D: e = launch_parts_##D(fmt, f32, a, p, st); break;
+    TACTKV_FOR_D(TACTKV_CASE)
+#undef TACTKV_CASE
+  }
+  if (e != cudaSuccess || p.count == 1) return e;
+  const dim3 grid(kTileRows, (unsigned)units);
+  if (f32) combine_kernel<true><<<grid, kThreads, 0, st>>>(a, p, tiles);
+  else combine_kernel<false><<<grid, kThreads, 0, st>>>(a, p, tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace text
+}  // namespace tactkv

@@ -614,7 +614,7 @@ def text_attention(q: torch.Tensor, cache: TextCache, page_table: torch.Tensor, 
             ptrs = tuple(x.data_ptr() for x in prior)
         batch = _text_batch(cache, page_table, kv_lens, row_starts, n_rows)
         if max_kv_len is None:
-            max_kv_len = min(page_table.shape[1] * cache.page_tokens, 2 ** 31 - 1)
+            max_kv_len = min(page_table.shape[1] * cache.page_tokens, 1 << 30)
         if workspace is None:
             workspace = text_workspace(cache, n_seqs=batch.n_seqs, n_rows=n_rows, max_rows=max_rows, q_heads=q_heads,
                                        max_kv_len=max_kv_len)
