@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     float z[2][4] = {};
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
+      float low[4] = {};                         // the queries' lower terms are summed apart: their rounding stays small
       const uint32_t k_top = Sh::kCoded ? __shfl_sync(~0u, top, 16 + 8 * n + r) : 0u;
 #pragma unroll
       for (int j = 0; j < Sh::kKVecs; ++j) {
@@ -356,9 +357,11 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
           if constexpr (Sh::kCoded) b[0] = mul_half2(b[0], f), b[1] = mul_half2(b[1], f);
 #pragma unroll
           for (int x = 0; x < Sh::kLimbs; ++x)
-            mma<kHalf>(z[n], q_frag[(x * (D / 16) + j * (Sh::kKElems / 4) + k) * 32 + lane], b[0], b[1]);
+            mma<kHalf>(x ? low : z[n], q_frag[(x * (D / 16) + j * (Sh::kKElems / 4) + k) * 32 + lane], b[0], b[1]);
         }
       }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) z[n][x] += low[x];
     }
     // z[n][0, 1]: row r, tokens 8n + 2c, 8n + 2c + 1;  z[n][2, 3]: row r + 8
 #pragma unroll

@@ -1,13 +1,16 @@
 """The text cache on the GPU against plain float64 (text_plain.py): appending, reading, attention, and a decode
 step that joins them with the visual tokens' compressed attention.
 
-Tolerances.  Codes, scale bytes and read values are exact.  Attention's out has
-  |error| <= h_out |out| + (h_p + 2^-15) A + 2^-22 max|V|,   A = sum p |V| / sum p,
+Tolerances.  Codes, scale bytes and read values are exact.  In attention a score is summed by D / 16 matrix
+instructions, each of which adds to a float32 with an error of at most one unit, 2^-23 of a sum that never exceeds
+S = sum |q k| / sqrt(D); the query's lower terms, the change to log2 and the scaling add less than four more, so
+  dz = (D / 16 + 4) 2^-23 S
+bounds a score's error, and exp(z) is off by 2 dz (its own error and the maximum's).  Exponentials and sums of
+at most 2^12 float32 terms (pairwise over lanes, warps and parts) stay within 2^-16.  So
+  |out error| <= h_out |out| + (h_p + 2 dz + 2^-16) A + 2^-22 max|V|,   A = sum p |V| / sum p,
 with h = eps / 2 of a type: h_out of the output, h_p of the probabilities as they multiply V (bfloat16 caches: 2^-8;
-coded ones: half precision, 2^-11; float32 queries: split, below 2^-20).  2^-15 covers float32: a score z has an
-error of a few 2^-24 of sum |q k| / sqrt(D) <= 2^6 here, so exp(z) one of 2^-16; exponentials and sums are within
-2^-18.  2^-22 max|V| covers what half precision drops below 2^-24 of its largest value.  m and l follow from the
-same bound on z: 2^-21 S, with S = max sum |q k| / sqrt(D), and relative 2^-20 S + 2^-17.
+coded ones: half precision, 2^-11; float32 queries: split, below 2^-20); 2^-22 max|V| covers what half precision
+drops below 2^-24 of its largest value.  |m error| <= dz + 2^-22 |m|, and |l error| <= (2 dz + 2^-16) l.
 """
 import math
 
@@ -116,13 +119,14 @@ def verify(s, q, words, pr, got, io):
         nan = np.isnan(rl)
         assert np.array_equal(np.isnan(l[sl]), nan)
         assert np.array_equal(np.isneginf(m[sl]), np.isneginf(rm))
-        tol = h_out * np.abs(ro) + (h_p + 2.0 ** -15) * mag + 2.0 ** -22 * big
+        dz = (s.D / 16 + 4) * 2.0 ** -23 * S
+        tol = h_out * np.abs(ro) + (h_p + 2 * dz + 2.0 ** -16)[..., None] * mag + 2.0 ** -22 * big
         bad = np.abs(out[sl] - ro) > tol
         bad[nan] = False
         assert not bad.any(), (i, np.argwhere(bad)[:4], out[sl][bad][:4], ro[bad][:4], tol[bad][:4])
         fin = np.isfinite(rm) & ~nan
-        assert (np.abs(m[sl] - rm)[fin] <= (2.0 ** -21 * S + 2.0 ** -22 * np.abs(np.where(fin, rm, 0)))[fin]).all()
-        assert (np.abs(l[sl] - rl)[~nan] <= ((2.0 ** -20 * S + 2.0 ** -17) * rl)[~nan]).all()
+        assert (np.abs(m[sl] - rm)[fin] <= (dz + 2.0 ** -22 * np.abs(np.where(fin, rm, 0)))[fin]).all()
+        assert (np.abs(l[sl] - rl)[~nan] <= ((2 * dz + 2.0 ** -16) * rl)[~nan]).all()
     end = s.starts()[-1]
     assert (got[0][end:] == 77.0).all()                  # rows behind the last sequence
 
@@ -392,7 +396,7 @@ def test_attention_reports_bad_rows_and_pages():
             seen = P.visible(2, 40, None)
             seen[:, 16:32] = False
             o, _, rl, _, S = P.attend(q[:2].double().cpu().numpy(), K, V, seen)
-            assert np.all(np.abs(l[:2].cpu().numpy() - rl) <= (2.0 ** -20 * S + 2.0 ** -17) * rl)
+            assert np.all(np.abs(l[:2].cpu().numpy() - rl) <= (2 * (D / 16 + 4) * 2.0 ** -23 * S + 2.0 ** -16) * rl)
         else:
             assert not out[:2].any() and torch.isneginf(m[:2]).all() and not l[:2].any()
 
