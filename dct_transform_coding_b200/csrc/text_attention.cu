@@ -16,6 +16,8 @@
 // are 2^-24 of the largest.  bfloat16 caches go in as they are.  Queries: bfloat16 ones are exact in
 // either type (scaled by a power of two for each row); float32 ones are split into two half-precision or
 // three bfloat16 terms, and so are the probabilities then.
+#include <atomic>
+
 #include "text_attention.cuh"
 
 #ifndef TACTKV_TEXT_D
@@ -594,7 +596,16 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
 template <int FMT, bool F32>
 cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
   using Sh = Shape<FMT, F32>;
-  cudaFuncSetAttribute(parts_kernel<FMT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  // the kernel's shared memory is set once for each device (twice by two threads at once does no harm)
+  static std::atomic<unsigned long long> set{0};
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    if (cudaError_t e = cudaFuncSetAttribute(parts_kernel<FMT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem))
+      return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int tiles = (a.max_rows * (a.q_heads / a.c.heads) + kTileRows - 1) / kTileRows;
   parts_kernel<FMT, F32><<<dim3(p.count, a.c.heads * tiles, a.b.n_seqs), kWarps * 32, Sh::kSmem, st>>>(a, p);
   return cudaGetLastError();

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence
 
 import torch
@@ -86,7 +87,7 @@ class tactkv_text_batch(ctypes.Structure):
 
 
 _P = ctypes.POINTER(tactkv_unit)
-_TC, _TB = ctypes.POINTER(tactkv_text_cache), ctypes.POINTER(tactkv_text_batch)
+_TC, _TB = ctypes.c_void_p, ctypes.c_void_p   # tactkv_text_cache and tactkv_text_batch, as addresses or packed bytes
 _lib.tactkv_payload_bytes.restype = ctypes.c_size_t
 _lib.tactkv_payload_bytes.argtypes = [_P]
 _lib.tactkv_workspace_bytes.restype = ctypes.c_size_t
@@ -438,6 +439,7 @@ class TextCache:
         self.device = k_pages.device
         self.struct = tactkv_text_cache(self.format, self.heads, self.head_dim, self.page_tokens, self.n_pages,
                                         *[x.data_ptr() for x in pools])
+        self.ptr = ctypes.addressof(self.struct)
         if tactkv_text_workspace_bytes(self, 0, 0, 0, 0, 0) == 0:
             raise TactkvError(TACTKV_UNSUPPORTED_SHAPE, "TextCache")
 
@@ -451,7 +453,7 @@ def text_cache(fmt: str, n_pages: int, heads: int, head_dim: int, *, page_tokens
 
 def tactkv_text_workspace_bytes(cache: TextCache, n_seqs: int, n_rows: int, q_heads: int, max_rows: int,
                                 max_kv_len: int) -> int:
-    return int(_lib.tactkv_text_workspace_bytes(cache.struct, n_seqs, n_rows, q_heads, max_rows, max_kv_len))
+    return int(_lib.tactkv_text_workspace_bytes(cache.ptr, n_seqs, n_rows, q_heads, max_rows, max_kv_len))
 
 
 def text_workspace(cache: TextCache, *, n_seqs: int, n_rows: int, max_rows: int = 1, q_heads: int = 0,
@@ -480,38 +482,33 @@ def text_tree(parents: Sequence[Sequence[int]], device="cuda") -> torch.Tensor:
     return torch.tensor(words, dtype=torch.int64, device=device)
 
 
+_TEXT_BATCH = struct.Struct("@PPPiii")   # tactkv_text_batch
+_TEXT_IO = {torch.bfloat16: 0, torch.float32: TACTKV_FP32_IO}
+
+
 def _text_batch(cache: TextCache, page_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
-                n_rows: int) -> tactkv_text_batch:
+                n_rows: int) -> bytes:
     n_seqs, max_pages = page_table.shape
     for x in (page_table, kv_lens, row_starts):
         if x.dtype != torch.int32 or not x.is_contiguous() or x.device != cache.device:
             raise ValueError("page_table, kv_lens and row_starts are contiguous int32 tensors on the cache's GPU")
     if kv_lens.numel() != n_seqs or row_starts.numel() != n_seqs + 1:
         raise ValueError("page_table [n_seqs, max_pages], kv_lens [n_seqs], row_starts [n_seqs + 1]")
-    return tactkv_text_batch(page_table.data_ptr(), kv_lens.data_ptr(), row_starts.data_ptr(), n_seqs, n_rows, max_pages)
+    return _TEXT_BATCH.pack(page_table.data_ptr(), kv_lens.data_ptr(), row_starts.data_ptr(), n_seqs, n_rows, max_pages)
 
 
-class _text_call:
-    """The device and stream of one call: what the wrapper allocates and converts belongs to that stream."""
+def _text_elsewhere(cache: TextCache, stream: Optional[torch.cuda.Stream]) -> bool:
+    """Whether a call needs another device or stream made current first.  What it allocates and converts then
+    belongs to the stream that it runs on."""
+    return stream is not None or torch.cuda.current_device() != cache.device.index
 
-    def __init__(self, cache: TextCache, stream: Optional[torch.cuda.Stream]):
-        self.ctx = None
-        if stream is not None:
-            if stream.device != cache.device:
-                raise ValueError("the stream is not on the cache's GPU")
-            self.ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != cache.device.index:
-            self.ctx = torch.cuda.device(cache.device)
-        self.device = cache.device
 
-    def __enter__(self) -> int:
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _text_there(cache: TextCache, stream: Optional[torch.cuda.Stream]):
+    if stream is None:
+        return torch.cuda.device(cache.device)
+    if stream.device != cache.device:
+        raise ValueError("the stream is not on the cache's GPU")
+    return torch.cuda.stream(stream)
 
 
 def _text_done(status: int, what: str, check: bool, workspace: torch.Tensor, stream_ptr: int) -> None:
@@ -523,19 +520,18 @@ def _text_done(status: int, what: str, check: bool, workspace: torch.Tensor, str
             raise TactkvError(ds, what + " (device)")
 
 
-_TEXT_IO = {torch.bfloat16: 0, torch.float32: TACTKV_FP32_IO}
-
-
 def _text_pair(cache: TextCache, k: torch.Tensor, v: torch.Tensor, write: bool):
-    """k and v [rows, heads, head_dim] with one pair of strides, as the library takes them."""
+    """k and v [rows, heads, head_dim] with one pair of strides, as the library takes them: (k, v, strides)."""
     if (k.dtype not in _TEXT_IO or v.dtype != k.dtype or k.dim() != 3 or v.shape != k.shape
             or k.shape[1:] != (cache.heads, cache.head_dim) or k.device != cache.device or v.device != cache.device):
         raise ValueError("k and v [rows, heads, head_dim] are bfloat16 or float32 tensors on the cache's GPU")
-    if k.stride() != v.stride() or k.stride(2) != 1 or k.stride(0) <= 0:
+    strides = k.stride()
+    if v.stride() != strides or strides[2] != 1 or strides[0] <= 0 or strides[0] % 2 or strides[1] % 2:
         if write:
-            raise ValueError("k and v have equal strides, and neighbouring values along head_dim")
-        k, v = k.contiguous(), v.contiguous()
-    return k, v
+            raise ValueError("k and v have equal even strides, and neighbouring values along head_dim")
+        k, v = (x.clone(memory_format=torch.contiguous_format) for x in (k, v))
+        strides = k.stride()
+    return k, v, strides
 
 
 def text_append(cache: TextCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -545,15 +541,22 @@ def text_append(cache: TextCache, k: torch.Tensor, v: torch.Tensor, page_table: 
     row_starts[s+1] are sequence s's newest tokens, at positions kv_lens[s] - n .. kv_lens[s] - 1 (kv_lens counts
     them).  page_table [n_seqs, max_pages], kv_lens and row_starts are int32 on the GPU.  With values, returns
     (k, v) as the cache now holds them (rows behind the last sequence are left unset)."""
-    with _text_call(cache, stream) as stream_ptr:
-        k, v = _text_pair(cache, k, v, False)
-        batch = _text_batch(cache, page_table, kv_lens, row_starts, k.shape[0])
-        out = (torch.empty(k.shape, dtype=k.dtype, device=k.device), torch.empty(k.shape, dtype=k.dtype, device=k.device)) if values else None
-        if workspace is None:
-            workspace = text_workspace(cache, n_seqs=0, n_rows=0)
-        st = _lib.tactkv_text_append(cache.struct, batch, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-                                     out[0].data_ptr() if values else None, out[1].data_ptr() if values else None,
-                                     _TEXT_IO[k.dtype], workspace.data_ptr(), workspace.numel(), stream_ptr)
+    if _text_elsewhere(cache, stream):
+        with _text_there(cache, stream):
+            return text_append(cache, k, v, page_table, kv_lens, row_starts, values=values, workspace=workspace, check=check)
+    k, v, strides = _text_pair(cache, k, v, False)
+    batch = _text_batch(cache, page_table, kv_lens, row_starts, k.shape[0])
+    out, kp, vp = None, None, None
+    if values:
+        out = (torch.empty_like(k, memory_format=torch.contiguous_format),
+               torch.empty_like(v, memory_format=torch.contiguous_format))
+        kp, vp = out[0].data_ptr(), out[1].data_ptr()
+    if workspace is None:
+        workspace = text_workspace(cache, n_seqs=0, n_rows=0)
+    stream_ptr = torch._C._cuda_getCurrentRawStream(cache.device.index)
+    st = _lib.tactkv_text_append(cache.ptr, batch, k.data_ptr(), v.data_ptr(), strides[0], strides[1], kp, vp,
+                                 _TEXT_IO[k.dtype], workspace.data_ptr(), workspace.numel(), stream_ptr)
+    if st or check:
         _text_done(st, "tactkv_text_append", check, workspace, stream_ptr)
     return out
 
@@ -564,18 +567,23 @@ def text_read(cache: TextCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
     """Read the newest row_starts[s+1] - row_starts[s] tokens of every sequence (all kv_lens[s] of them, if that is
     as many): (k, v) [n_rows, heads, head_dim], into the pair out if given (rows behind the last sequence are
     left as they are)."""
-    with _text_call(cache, stream) as stream_ptr:
-        if out is None:
-            shape = (n_rows, cache.heads, cache.head_dim)
-            out = (torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device))
-        k, v = _text_pair(cache, *out, True)
-        if k.shape[0] != n_rows:
-            raise ValueError("out holds n_rows rows")
-        batch = _text_batch(cache, page_table, kv_lens, row_starts, n_rows)
-        if workspace is None:
-            workspace = text_workspace(cache, n_seqs=0, n_rows=0)
-        st = _lib.tactkv_text_read(cache.struct, batch, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-                                   _TEXT_IO[k.dtype], workspace.data_ptr(), workspace.numel(), stream_ptr)
+    if _text_elsewhere(cache, stream):
+        with _text_there(cache, stream):
+            return text_read(cache, page_table, kv_lens, row_starts, n_rows=n_rows, dtype=dtype, out=out,
+                             workspace=workspace, check=check)
+    if out is None:
+        k = torch.empty(n_rows, cache.heads, cache.head_dim, dtype=dtype, device=cache.device)
+        out = (k, torch.empty_like(k))
+    k, v, strides = _text_pair(cache, out[0], out[1], True)
+    if k.shape[0] != n_rows:
+        raise ValueError("out holds n_rows rows")
+    batch = _text_batch(cache, page_table, kv_lens, row_starts, n_rows)
+    if workspace is None:
+        workspace = text_workspace(cache, n_seqs=0, n_rows=0)
+    stream_ptr = torch._C._cuda_getCurrentRawStream(cache.device.index)
+    st = _lib.tactkv_text_read(cache.ptr, batch, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
+                               _TEXT_IO[k.dtype], workspace.data_ptr(), workspace.numel(), stream_ptr)
+    if st or check:
         _text_done(st, "tactkv_text_read", check, workspace, stream_ptr)
     return out
 
@@ -592,36 +600,47 @@ def text_attention(q: torch.Tensor, cache: TextCache, page_table: torch.Tensor, 
     queries' attention over other tokens, as attention_decode returns it (float32).  Returns (out, m, l): out
     like q; m and l float32 [rows, q_heads], the scores' maximum and exp-sum with the prior's.  Rows behind the last
     sequence are left as they are."""
-    with _text_call(cache, stream) as stream_ptr:
-        if q.dtype not in _TEXT_IO or q.dim() != 3 or q.shape[2] != cache.head_dim or q.device != cache.device:
-            raise ValueError("q [rows, q_heads, head_dim] is a bfloat16 or float32 tensor on the cache's GPU")
-        n_rows, q_heads, D = q.shape
-        if q.stride(2) != 1 or q.stride(0) % 8 or q.stride(1) % 8 or q.data_ptr() % 16:
-            q = q.clone(memory_format=torch.contiguous_format)
-        if out is None:
-            out = torch.empty((n_rows, q_heads, D), dtype=q.dtype, device=q.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
-            raise ValueError("out is a contiguous tensor of q's shape, type and device")
-        ml = torch.empty((2, n_rows, q_heads), dtype=torch.float32, device=q.device)
-        if tree is not None and (tree.dtype != torch.int64 or tree.numel() != n_rows or not tree.is_contiguous()
-                                 or tree.device != q.device):
+    if _text_elsewhere(cache, stream):
+        with _text_there(cache, stream):
+            return text_attention(q, cache, page_table, kv_lens, row_starts, max_rows=max_rows, max_kv_len=max_kv_len,
+                                  tree=tree, prior=prior, out=out, workspace=workspace, check=check)
+    device = cache.device
+    shape = q.shape
+    if q.dtype not in _TEXT_IO or len(shape) != 3 or shape[2] != cache.head_dim or q.device != device:
+        raise ValueError("q [rows, q_heads, head_dim] is a bfloat16 or float32 tensor on the cache's GPU")
+    n_rows, q_heads, D = shape
+    strides = q.stride()
+    if strides[2] != 1 or strides[0] % 8 or strides[1] % 8 or q.data_ptr() % 16:
+        q = q.clone(memory_format=torch.contiguous_format)
+        strides = q.stride()
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != device:
+        raise ValueError("out is a contiguous tensor of q's shape, type and device")
+    m = torch.empty(n_rows, q_heads, dtype=torch.float32, device=device)
+    l = torch.empty_like(m)
+    tree_ptr = None
+    if tree is not None:
+        if tree.dtype != torch.int64 or tree.numel() != n_rows or not tree.is_contiguous() or tree.device != device:
             raise ValueError("tree holds an int64 word for each row")
-        ptrs = (None, None, None)
-        if prior is not None:
-            for x, shape in zip(prior, ((n_rows, q_heads, D), (n_rows, q_heads), (n_rows, q_heads))):
-                if x.shape != shape or x.dtype != torch.float32 or not x.is_contiguous() or x.device != q.device:
-                    raise ValueError("prior = (out, m, l): contiguous float32 [rows, q_heads, head_dim], [rows, q_heads] (twice)")
-            ptrs = tuple(x.data_ptr() for x in prior)
-        batch = _text_batch(cache, page_table, kv_lens, row_starts, n_rows)
-        if max_kv_len is None:
-            max_kv_len = min(page_table.shape[1] * cache.page_tokens, 1 << 30)
-        if workspace is None:
-            workspace = text_workspace(cache, n_seqs=batch.n_seqs, n_rows=n_rows, max_rows=max_rows, q_heads=q_heads,
-                                       max_kv_len=max_kv_len)
-        m, l = ml
-        st = _lib.tactkv_text_attention(cache.struct, batch, q_heads, max_rows, max_kv_len, q.data_ptr(), q.stride(0),
-                                        q.stride(1), None if tree is None else tree.data_ptr(), *ptrs, out.data_ptr(),
-                                        m.data_ptr(), l.data_ptr(), _TEXT_IO[q.dtype], workspace.data_ptr(),
-                                        workspace.numel(), stream_ptr)
+        tree_ptr = tree.data_ptr()
+    po = pm = pl = None
+    if prior is not None:
+        po, pm, pl = prior
+        if (po.shape != shape or pm.shape != m.shape or pl.shape != m.shape
+                or any(x.dtype != torch.float32 or not x.is_contiguous() or x.device != device for x in prior)):
+            raise ValueError("prior = (out, m, l): contiguous float32 [rows, q_heads, head_dim], [rows, q_heads] (twice)")
+        po, pm, pl = po.data_ptr(), pm.data_ptr(), pl.data_ptr()
+    batch = _text_batch(cache, page_table, kv_lens, row_starts, n_rows)
+    if max_kv_len is None:
+        max_kv_len = min(page_table.shape[1] * cache.page_tokens, 1 << 30)
+    if workspace is None:
+        workspace = text_workspace(cache, n_seqs=page_table.shape[0], n_rows=n_rows, max_rows=max_rows, q_heads=q_heads,
+                                   max_kv_len=max_kv_len)
+    stream_ptr = torch._C._cuda_getCurrentRawStream(device.index)
+    st = _lib.tactkv_text_attention(cache.ptr, batch, q_heads, max_rows, max_kv_len, q.data_ptr(), strides[0],
+                                    strides[1], tree_ptr, po, pm, pl, out.data_ptr(), m.data_ptr(), l.data_ptr(),
+                                    _TEXT_IO[q.dtype], workspace.data_ptr(), workspace.numel(), stream_ptr)
+    if st or check:
         _text_done(st, "tactkv_text_attention", check, workspace, stream_ptr)
     return out, m, l

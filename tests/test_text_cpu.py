@@ -1,6 +1,4 @@
 """The text cache's host side without a GPU: sizes, refusals and the tree words (no kernel is launched)."""
-import ctypes
-
 import pytest
 
 import text_plain as P
@@ -17,13 +15,13 @@ def cache(T, **kw):
     d = dict(format=T.TACTKV_TEXT_MXFP8, heads=2, head_dim=64, page_tokens=16, n_pages=4, k_pages=4096, v_pages=8192,
              k_scales=16384, v_scales=32768)
     d.update(kw)
-    return T.tactkv_text_cache(**d)
+    return bytes(T.tactkv_text_cache(**d))
 
 
 def batch(T, **kw):
     d = dict(page_table=4096, kv_lens=4096, row_starts=4096, n_seqs=1, n_rows=1, max_pages=2)
     d.update(kw)
-    return T.tactkv_text_batch(**d)
+    return bytes(T.tactkv_text_batch(**d))
 
 
 BAD_CACHE = [
@@ -123,7 +121,13 @@ def test_workspace_sizes(T):
     assert size(-1, 0, 0, 0, 0) == 0 and size(0, 0, -1, 0, 0) == 0
     need = size(8, 8, 4, 1, 1 << 20)
     assert attend(T, c, batch(T, n_seqs=8, n_rows=8), length=1 << 20, n=need - 1) == T.TACTKV_WORKSPACE
-    assert T._lib.tactkv_text_workspace_bytes(ctypes.POINTER(T.tactkv_text_cache)(), 1, 1, 1, 1, 1) == 0
+    assert T._lib.tactkv_text_workspace_bytes(None, 1, 1, 1, 1, 1) == 0
+
+
+def test_packed_batch_is_the_structure(T):
+    b = T.tactkv_text_batch(11, 22, 33, 4, 5, 6)
+    assert T._TEXT_BATCH.pack(11, 22, 33, 4, 5, 6) == bytes(b)[:T._TEXT_BATCH.size]
+    assert bytes(b)[T._TEXT_BATCH.size:].strip(b"\0") == b""
 
 
 def test_tree_words(T):
