@@ -3,12 +3,14 @@
 //   s_t = q . K[t] / sqrt(D) over the tokens t that the row sees,  m = max s_t,  l = sum exp(s_t - m),
 //   out = (sum exp(s_t - m) V[t]) / l,  in one pass over the tokens with a running maximum and sum.
 //
-// A CTA has 16 rows (query heads of one K/V head, row = node * G + head within the group) of one sequence
-// and one part of its tokens.  Its warps take 16 tokens at a time each and never wait for one another: a
-// warp's two m16n8k16 products QK^T and PV take K and V as B fragments, and because the order of the
-// summed index is free, the fragment a lane needs is a piece of a row as it lies in the cache.  So each lane
-// copies its own pieces (cp.async, 16 bytes where head_dim allows) into a ring in shared memory and reads
-// back only those: no transposition and no barrier but the warp's own.
+// A CTA has a unit (sequence, K/V head and a tile of 8 NR rows; row = node * G + query head within the group)
+// and a part of the sequence's tokens.  Its warps take 16 tokens at a time each and never wait for one another.
+// The products are taken with the tokens, or the output's columns, as the m16n8k16 instruction's 16 and the
+// rows as its 8: S^T = K Q^T and O^T = V^T P^T.  A decode step's few rows then fill the instruction, K and
+// V are decoded once for all rows of the tile, and because the order of a summed index is free, the pieces of K
+// and V that a lane needs are pieces of rows as they lie in the cache.  So each lane copies its own
+// pieces (cp.async, 16 bytes where head_dim allows) into a ring in shared memory and reads back only those: no
+// barrier but the warp's own.  S^T's accumulators become P^T's fragments by one 8 x 8 transposition (movmatrix).
 //
 // Codes become half precision exactly, scaled by 2^(s - smax) with smax the token's largest scale: in
 // K, 2^smax multiplies the token's score; in V it multiplies the token's probability, relative to the largest
@@ -47,9 +49,10 @@ constexpr int vec_bytes(int bytes, int most) {   // the widest power of two that
   return v;
 }
 
-template <int FMT, bool F32>
+template <int FMT, bool F32, int NR>
 struct Shape {
   static constexpr bool kCoded = FMT != kBf16;
+  static constexpr int kRows = 8 * NR;
   static constexpr int kRow = D * code_bits(FMT) / 8;
   static constexpr int kKVec = vec_bytes(kRow / 4, 16), kKVecs = kRow / 4 / kKVec;    // a lane's pieces of a K row
   static constexpr int kVVec = vec_bytes(kRow / 8, 16), kVVecs = kRow / 8 / kVVec;    // and of a V row
@@ -61,11 +64,12 @@ struct Shape {
   static constexpr int kStagesFit = 17920 / kStage;
   static constexpr int kStages = kStagesFit < 3 ? 3 : (kStagesFit > 8 ? 8 : kStagesFit);
   static constexpr int kLimbs = !F32 ? 1 : (kCoded ? 2 : 3);
-  static constexpr int kQBytes = kLimbs * (D / 16) * 32 * 16;
+  static constexpr bool kQInRegs = 2 * NR * kLimbs * (D / 16) <= 32;
+  static constexpr int kQBytes = NR * kLimbs * (D / 16) * 32 * 8;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kSum = kWarps * 16 * (D + 4) * 4;          // the warps' sums, over the ring when it is done
+  static constexpr int kSum = kWarps * kRows * (D + 4) * 4;       // the warps' sums, over the ring when it is done
   static constexpr int kBody = kRing > kSum ? kRing : kSum;
-  static constexpr int kSmem = kQBytes + kBody + kWarps * 16 * 8;
+  static constexpr int kSmem = kQBytes + kBody + kRows * 8 + kRows * 4 + kWarps * kRows * 8;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -95,15 +99,20 @@ __device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)
 }
 
 template <bool HALF>
-__device__ __forceinline__ void mma(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint2 b) {
   if constexpr (HALF)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 matrix of 16-bit values across the warp
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(v));
+  return y;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 for -inf
@@ -151,15 +160,18 @@ __device__ __forceinline__ bool odd2(uint32_t v) {
   return (v & e) == e || (v >> 16 & e) == e;
 }
 
-template <int FMT, bool F32>
+template <int FMT, bool F32, int NR>
 __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, const Parts parts) {
-  using Sh = Shape<FMT, F32>;
+  using Sh = Shape<FMT, F32, NR>;
   constexpr bool kHalf = Sh::kCoded;
-  constexpr int NT = D / 8;                       // column tiles of the output
+  constexpr int MT = D / 16;                      // 16-column tiles of the output
+  constexpr int KS = D / 16;                      // K's steps
   extern __shared__ __align__(16) unsigned char smem[];
-  uint4* q_frag = reinterpret_cast<uint4*>(smem);                                 // [limb][D / 16][lane]
+  uint2* q_frag = reinterpret_cast<uint2*>(smem);                                 // [limb][step][tile][lane]
   unsigned char* body = smem + Sh::kQBytes;
-  float2* sums = reinterpret_cast<float2*>(body + Sh::kBody);                     // [warp][16] (m, l)
+  unsigned long long* words = reinterpret_cast<unsigned long long*>(body + Sh::kBody);   // [row] what it sees
+  float* row_factors = reinterpret_cast<float*>(words + Sh::kRows);
+  float2* sums = reinterpret_cast<float2*>(row_factors + Sh::kRows);              // [warp][row] (m, l)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = lane / 4, c = lane & 3;
   const int G = a.q_heads / a.c.heads;
@@ -178,68 +190,9 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     }
     return;
   }
-  const int M = sp.rows * G, row0 = tile * kTileRows, before = sp.len - sp.rows;
+  const int M = sp.rows * G, row0 = tile * Sh::kRows, before = sp.len - sp.rows;
   const int t0 = part * parts.tokens, t1 = t0 + min(sp.len - t0, parts.tokens);
   if (row0 >= M || (part > 0 && t0 >= sp.len)) return;
-
-  // ---- the queries' A fragments ----
-  // Lane (r, c) of K's step k holds elements idx = 4k .. 4k+3 of its share of row r: d = (idx / kKElems * 4
-  // + c) * kKElems + idx % kKElems.  Rows are scaled so that their largest element is in [2^14, 2^15).
-  float row_factor[2] = {1.f, 1.f};
-  {
-    const long long base = (long long)sp.first * a.q_token + (long long)head * G * a.q_head;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = row0 + r + 8 * h;
-      const bool in = row < M;
-      const long long at = base + (in ? (long long)(row / G) * a.q_token + (long long)(row % G) * a.q_head : 0);
-      float f = 1.f;
-      if constexpr (kHalf) {
-        uint32_t top = 0;
-        for (int i = c; i < D / 2; i += 4) {
-          float2 v;
-          if constexpr (F32) v = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + 2 * i);
-          else v = unpack_bf16x2(*reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + at + 2 * i));
-          top = max(top, max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu));
-        }
-        top = max(top, __shfl_xor_sync(~0u, top, 1));
-        top = max(top, __shfl_xor_sync(~0u, top, 2));
-        const int E = (int)(top >> 23);                       // biased; f = 2^(14 + 127 - E) within float32's range
-        const int e = E == 255 || top == 0 ? 0 : max(-126, min(126, 141 - E));
-        f = __uint_as_float((uint32_t)(127 + e) << 23);
-        row_factor[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-      }
-      for (int k = warp; k < D / 16; k += kWarps) {
-        float x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int idx = 4 * k + i, d = (idx / Sh::kKElems * 4 + c) * Sh::kKElems + idx % Sh::kKElems;
-          x[i] = !in ? 0.f
-                 : F32 ? static_cast<const float*>(a.q)[at + d]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + d]);
-          if constexpr (kHalf) x[i] *= f;
-        }
-#pragma unroll
-        for (int n = 0; n < Sh::kLimbs; ++n) {
-          const uint32_t lo = pack2<kHalf>(x[0], x[1]), hi = pack2<kHalf>(x[2], x[3]);
-          uint32_t* to = reinterpret_cast<uint32_t*>(q_frag + (n * (D / 16) + k) * 32 + lane);
-          to[h] = lo, to[2 + h] = hi;
-          const float2 u = unpack2<kHalf>(lo), v = unpack2<kHalf>(hi);
-          x[0] -= u.x, x[1] -= u.y, x[2] -= v.x, x[3] -= v.y;
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) row_factor[h] *= kToLog2;
-  // Which of the sequence's own rows each of the lane's two rows sees.
-  unsigned long long word[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int node = min((row0 + r + 8 * h) / G, sp.rows - 1);
-    word[h] = a.tree ? a.tree[sp.first + node] : (node >= 63 ? ~0ull : (2ull << node) - 1);
-  }
-  __syncthreads();
 
   // ---- the ring ----
   unsigned char* ring = body + warp * (Sh::kStages * Sh::kStage);
@@ -284,7 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
                                  vs + tok * Sh::kRow + (j * 8 + (Sh::kVVec < 4 ? r & ~1 : r)) * Sh::kVVec, there);
       }
       if constexpr (Sh::kCoded) {
-        // 16 tokens' scales are D / 2 neighbouring bytes: lanes 0 .. copy K's, the next ones V's, 16 at a time
+        // 16 tokens' scales are D / 2 neighbouring bytes: the first lanes copy K's, the next ones V's, 16 at a time
         if (lane < D / 16) {
           const int kv = lane >= D / 32, i16 = lane - kv * (D / 32);
           copy_async<16>(to + Sh::kKBytes + Sh::kVBytes + kv * Sh::kScaleBytes + 16 * i16,
@@ -297,16 +250,86 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
 #pragma unroll
   for (int i = 0; i < Sh::kStages - 1; ++i) issue(i, __shfl_sync(~0u, pages, i));
 
-  float o[NT][4] = {};
-  float m_ref[2] = {-INFINITY, -INFINITY}, m_true[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  int ref = 0;                                   // the largest V scale so far (coded caches)
+  // ---- the queries' B fragments ----
+  // Lane (r, c) of K's step k holds elements idx = 4k .. 4k+3 of its share of row 8n + r: d = (idx / kKElems * 4
+  // + c) * kKElems + idx % kKElems.  For coded caches rows are scaled so that their largest element is in
+  // [2^14, 2^15).
+  for (int n = warp; n < NR; n += kWarps) {
+    const int row = row0 + 8 * n + r;
+    const bool in = row < M;
+    const int node = in ? row / G : 0;
+    const long long at = (long long)(sp.first + node) * a.q_token + (long long)(head * G + (in ? row % G : 0)) * a.q_head;
+    float x[KS][4];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int d = (4 * k / Sh::kKElems * 4 + c) * Sh::kKElems + 4 * k % Sh::kKElems;
+      if constexpr (F32) {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + d);
+        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at + d);
+        const float2 lo = unpack_bf16x2(v.x), hi = unpack_bf16x2(v.y);
+        x[k][0] = lo.x, x[k][1] = lo.y, x[k][2] = hi.x, x[k][3] = hi.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!in) x[k][i] = 0.f;
+        top = max(top, __float_as_uint(x[k][i]) & 0x7FFFFFFFu);
+      }
+    }
+    float f = 1.f, back = kToLog2;
+    if constexpr (kHalf) {
+      top = max(top, __shfl_xor_sync(~0u, top, 1));
+      top = max(top, __shfl_xor_sync(~0u, top, 2));
+      const int E = (int)(top >> 23);                         // biased; f = 2^(14 + 127 - E) within float32's range
+      const int e = E == 255 || top == 0 ? 0 : max(-126, min(126, 141 - E));
+      f = __uint_as_float((uint32_t)(127 + e) << 23);
+      back *= __uint_as_float((uint32_t)(127 - e) << 23);
+    }
+    if (c == 0) {
+      row_factors[8 * n + r] = back;
+      words[8 * n + r] = a.tree ? a.tree[sp.first + node] : (node >= 63 ? ~0ull : (2ull << node) - 1);
+    }
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[k][i] *= f;
+#pragma unroll
+      for (int y = 0; y < Sh::kLimbs; ++y) {
+        const uint2 w = make_uint2(pack2<kHalf>(x[k][0], x[k][1]), pack2<kHalf>(x[k][2], x[k][3]));
+        q_frag[((y * KS + k) * NR + n) * 32 + lane] = w;
+        const float2 u = unpack2<kHalf>(w.x), v = unpack2<kHalf>(w.y);
+        x[k][0] -= u.x, x[k][1] -= u.y, x[k][2] -= v.x, x[k][3] -= v.y;
+      }
+    }
+  }
+  __syncthreads();
+  uint2 q_reg[Sh::kQInRegs ? Sh::kLimbs * KS * NR : 1];
+  if constexpr (Sh::kQInRegs) {
+#pragma unroll
+    for (int i = 0; i < Sh::kLimbs * KS * NR; ++i) q_reg[i] = q_frag[i * 32 + lane];
+  }
+  float row_factor[NR][2];                        // the lane's scores are of rows 8n + 2c and 8n + 2c + 1
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) row_factor[n][x] = row_factors[8 * n + 2 * c + x];
+
+  float o[MT][NR][4] = {};                        // columns r (0, 1) and r + 8 (2, 3) of a tile; rows 2c, 2c + 1
+  float m_ref[NR][2], m_true[NR][2], l[NR][2] = {};
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) m_ref[n][x] = m_true[n][x] = -INFINITY;
+  uint32_t ref = 0;                               // the largest V scale so far (coded caches)
 
   for (int i = 0; i < steps; ++i) {
     if (i && i % 32 == 0) pages = pages_next, pages_next = page_of(i + 32 + lane);
     copy_wait<Sh::kStages - 2>();
     __syncwarp();
     {
-      const int n = i + Sh::kStages - 1;         // its slot is the one of step i - 1, which every lane has left
+      const int n = i + Sh::kStages - 1;          // its slot is the one of step i - 1, which every lane has left
       const int pa = __shfl_sync(~0u, pages, n & 31), pb = __shfl_sync(~0u, pages_next, n & 31);
       issue(n, n / 32 == i / 32 ? pa : pb);
     }
@@ -316,6 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     const unsigned char* k_scales = stage + Sh::kKBytes + Sh::kVBytes;
     const unsigned char* v_scales = k_scales + Sh::kScaleBytes;
     const int t = (first + i * kWarps) * kStep;
+    const int held = sp.len - t;
 
     // Lane x < 16 finds the largest scale of token x in V, lane 16 + x in K (the NaN scale aside).
     uint32_t top = 0;
@@ -326,132 +350,140 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
         const uint32_t s = src[g];
         top = max(top, s == 255u ? 0u : s);
       }
-      if ((lane & 15) >= sp.len - t) top = 0;     // what the page holds behind the last token
+      if ((lane & 15) >= held) top = 0;           // what the page holds behind the last token
     }
 
-    // ---- scores ----
-    float z[2][4] = {};
+    // ---- scores: z[n][0, 1]: token r, rows 8n + 2c, + 1;  z[n][2, 3]: token r + 8 ----
+    float z[NR][4] = {};
+    uint32_t k_top[2] = {};
+    {
+      float low[NR][4] = {};                      // the queries' lower terms are summed apart: their rounding stays small
+      uint32_t w[2][Sh::kKVecs][4], f[2][Sh::kKVecs];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      float low[4] = {};                         // the queries' lower terms are summed apart: their rounding stays small
-      const uint32_t k_top = Sh::kCoded ? __shfl_sync(~0u, top, 16 + 8 * n + r) : 0u;
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (Sh::kCoded) k_top[h] = __shfl_sync(~0u, top, 16 + 8 * h + r);
 #pragma unroll
-      for (int j = 0; j < Sh::kKVecs; ++j) {
-        uint32_t w[4];
-        load_words<Sh::kKVec>(stage + ((n * Sh::kKVecs + j) * 32 + lane) * Sh::kKVec, w);
-        uint32_t f = 0;
-        if constexpr (Sh::kCoded) {
-          f = half_factor(k_scales[(8 * n + r) * (D / kGroup) + (j * 4 + c) * Sh::kKElems / kGroup], k_top);
-          f |= f << 16;
+        for (int j = 0; j < Sh::kKVecs; ++j) {
+          load_words<Sh::kKVec>(stage + ((h * Sh::kKVecs + j) * 32 + lane) * Sh::kKVec, w[h][j]);
+          if constexpr (Sh::kCoded)
+            f[h][j] = half_factor(k_scales[(8 * h + r) * (D / kGroup) + (j * 4 + c) * Sh::kKElems / kGroup], k_top[h]) * 0x10001u;
         }
+      }
+#pragma unroll
+      for (int j = 0; j < Sh::kKVecs; ++j)
 #pragma unroll
         for (int k = 0; k < Sh::kKElems / 4; ++k) {
-          uint32_t b[2];
-          if constexpr (FMT == kBf16) {
-            b[0] = w[2 * k], b[1] = w[2 * k + 1];
-          } else if constexpr (FMT == kFp8) {
-            unpack_e4m3x4(w[k], b[0], b[1]);
-          } else {
-            uint32_t h[4];
-            unpack_e2m1x8(w[k / 2], h);
-            b[0] = h[k % 2 * 2], b[1] = h[k % 2 * 2 + 1];
+          uint32_t b[4];                          // A fragment: token r, r + 8 (elements 0, 1), token r, r + 8 (2, 3)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (FMT == kBf16) {
+              b[h] = w[h][j][2 * k], b[2 + h] = w[h][j][2 * k + 1];
+            } else if constexpr (FMT == kFp8) {
+              unpack_e4m3x4(w[h][j][k], b[h], b[2 + h]);
+            } else {
+              uint32_t u[4];
+              unpack_e2m1x8(w[h][j][k / 2], u);
+              b[h] = u[k % 2 * 2], b[2 + h] = u[k % 2 * 2 + 1];
+            }
+            if constexpr (Sh::kCoded) b[h] = mul_half2(b[h], f[h][j]), b[2 + h] = mul_half2(b[2 + h], f[h][j]);
           }
-          if constexpr (Sh::kCoded) b[0] = mul_half2(b[0], f), b[1] = mul_half2(b[1], f);
+          const int step = j * (Sh::kKElems / 4) + k;
 #pragma unroll
-          for (int x = 0; x < Sh::kLimbs; ++x)
-            mma<kHalf>(x ? low : z[n], q_frag[(x * (D / 16) + j * (Sh::kKElems / 4) + k) * 32 + lane], b[0], b[1]);
+          for (int y = 0; y < Sh::kLimbs; ++y)
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              const int at = (y * KS + step) * NR + n;
+              uint2 q;
+              if constexpr (Sh::kQInRegs) q = q_reg[at];
+              else q = q_frag[at * 32 + lane];
+              // odd steps go into the second sum (without lower terms): two chains of dependent products
+              mma<kHalf>(y || (Sh::kLimbs == 1 && step % 2) ? low[n] : z[n], b, q);
+            }
         }
-      }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) z[n][x] += low[x];
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          z[n][x] += low[n][x];
+          z[n][x] *= (Sh::kCoded ? scale_value(k_top[x / 2]) : 1.f) * row_factor[n][x % 2];
+        }
     }
-    // z[n][0, 1]: row r, tokens 8n + 2c, 8n + 2c + 1;  z[n][2, 3]: row r + 8
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float f = Sh::kCoded ? scale_value(__shfl_sync(~0u, top, 16 + 8 * n + 2 * c + x)) : 1.f;
-        z[n][x] *= f * row_factor[0], z[n][2 + x] *= f * row_factor[1];
-      }
     const bool tail = t + kStep > before;
     if (tail) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int node = t + 8 * n + 2 * c + x - before;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (node >= 0 && (node >= sp.rows || !(word[h] >> node & 1))) z[n][2 * h + x] = -INFINITY;
+        for (int x = 0; x < 4; ++x) {
+          const int node = t + r + 8 * (x / 2) - before;
+          if (node >= 0 && (node >= sp.rows || !(words[8 * n + 2 * c + x % 2] >> node & 1))) z[n][x] = -INFINITY;
         }
     }
 
-    // ---- running maximum ----
+    // ---- running maximum: moved only when a score is 2^kSlack above it ----
     bool over = false;
-    float high[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      high[h] = fmaxf(fmaxf(z[0][2 * h], z[0][2 * h + 1]), fmaxf(z[1][2 * h], z[1][2 * h + 1]));
-      m_true[h] = fmaxf(m_true[h], high[h]);
-      over |= high[h] > m_ref[h] + kSlack;
-    }
-    uint32_t new_ref = ref;
-    if constexpr (Sh::kCoded) new_ref = max((uint32_t)ref, __reduce_max_sync(~0u, lane < 16 ? top : 0u));
-    if (__any_sync(~0u, over) || new_ref != ref) {
-      const float down = Sh::kCoded ? __uint_as_float((uint32_t)max(127 + ref - (int)new_ref, 0) << 23) : 1.f;
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v = fmaxf(high[h], __shfl_xor_sync(~0u, high[h], 1));
-        v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
-        const float next = v > m_ref[h] + kSlack ? v : m_ref[h];
-        const float keep = next == -INFINITY ? 1.f : exp2_fast(m_ref[h] - next);
-        m_ref[h] = next;
-        l[h] *= keep;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][2 * h] *= keep * down, o[n][2 * h + 1] *= keep * down;
+      for (int x = 0; x < 2; ++x) {
+        const float high = fmaxf(z[n][x], z[n][2 + x]);
+        m_true[n][x] = fmaxf(m_true[n][x], high);
+        over |= high > m_ref[n][x] + kSlack;
       }
+    uint32_t new_ref = ref;
+    if constexpr (Sh::kCoded) new_ref = max(ref, __reduce_max_sync(~0u, lane < 16 ? top : 0u));
+    if (__any_sync(~0u, over) || new_ref != ref) {
+      const float down = Sh::kCoded ? __uint_as_float((uint32_t)max(127 + (int)ref - (int)new_ref, 0) << 23) : 1.f;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float v = fmaxf(z[n][x], z[n][2 + x]);
+#pragma unroll
+          for (int y = 4; y <= 16; y *= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, y));
+          const float next = v > m_ref[n][x] + kSlack ? v : m_ref[n][x];
+          const float keep = next == -INFINITY ? 1.f : exp2_fast(m_ref[n][x] - next);
+          m_ref[n][x] = next;
+          l[n][x] *= keep;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) o[mt][n][x] *= keep * down, o[mt][n][2 + x] *= keep * down;
+        }
       ref = new_ref;
     }
 
-    // ---- probabilities: the lane's tokens 2c, 2c + 1, 8 + 2c, 8 + 2c + 1 of rows r and r + 8 ----
-    float p[2][4];                                // [h][token]
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float shift = kBase - (m_ref[h] == -INFINITY ? 0.f : m_ref[h]);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) p[h][n] = exp2_fast(z[n / 2][2 * h + n % 2] + shift);
-      l[h] += (p[h][0] + p[h][1]) + (p[h][2] + p[h][3]);
-    }
-    uint32_t v_top[4];
-    if constexpr (Sh::kCoded) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        v_top[n] = __shfl_sync(~0u, top, 2 * c + (n & 1) + 8 * (n >> 1));
-        const float f = __uint_as_float((uint32_t)max(127 + (int)v_top[n] - ref, 0) << 23);
-        p[0][n] *= f, p[1][n] *= f;
-      }
-    }
-    uint4 pa[Sh::kLimbs];
+    // ---- probabilities, and their B fragments: tokens 2c, 2c + 1 (x) and 2c + 8, 2c + 9 (y) of row 8n + r ----
+    float p[NR][4];
+    uint2 pb[Sh::kLimbs][NR];
     {
-      float x[2][4];
+      float fold[2] = {1.f, 1.f};
+      if constexpr (Sh::kCoded) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
+          fold[h] = __uint_as_float((uint32_t)max(127 + (int)__shfl_sync(~0u, top, 8 * h + r) - (int)ref, 0) << 23);
+      }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) x[h][n] = p[h][n];
+      for (int n = 0; n < NR; ++n) {
 #pragma unroll
-      for (int n = 0; n < Sh::kLimbs; ++n) {
-        pa[n] = make_uint4(pack2<kHalf>(x[0][0], x[0][1]), pack2<kHalf>(x[1][0], x[1][1]),
-                           pack2<kHalf>(x[0][2], x[0][3]), pack2<kHalf>(x[1][2], x[1][3]));
-        if (n + 1 < Sh::kLimbs) {
-          const float2 u0 = unpack2<kHalf>(pa[n].x), u1 = unpack2<kHalf>(pa[n].y), u2 = unpack2<kHalf>(pa[n].z),
-                       u3 = unpack2<kHalf>(pa[n].w);
-          x[0][0] -= u0.x, x[0][1] -= u0.y, x[1][0] -= u1.x, x[1][1] -= u1.y;
-          x[0][2] -= u2.x, x[0][3] -= u2.y, x[1][2] -= u3.x, x[1][3] -= u3.y;
+        for (int x = 0; x < 4; ++x)
+          p[n][x] = exp2_fast(z[n][x] + (kBase - (m_ref[n][x % 2] == -INFINITY ? 0.f : m_ref[n][x % 2])));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) l[n][x] += p[n][x] + p[n][2 + x];
+        float u[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if constexpr (Sh::kCoded) p[n][x] *= fold[x / 2];
+          u[x] = p[n][x];
+        }
+#pragma unroll
+        for (int y = 0; y < Sh::kLimbs; ++y) {
+          const uint32_t lo = pack2<kHalf>(u[0], u[1]), hi = pack2<kHalf>(u[2], u[3]);
+          pb[y][n] = make_uint2(transpose8(lo), transpose8(hi));
+          const float2 v = unpack2<kHalf>(lo), w = unpack2<kHalf>(hi);
+          u[0] -= v.x, u[1] -= v.y, u[2] -= w.x, u[3] -= w.y;
         }
       }
     }
 
-    // ---- sums: column r of tile (j, e) is d = (j * 8 + r) * kVElems + e ----
+    // ---- sums: column r of half tile (j, e) is d = (j * 8 + r) * kVElems + e ----
 #pragma unroll
     for (int j = 0; j < Sh::kVVecs; ++j) {
       uint32_t w[4][4], f01 = 0, f23 = 0;
@@ -466,7 +498,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
         for (int n = 0; n < 4; ++n) {
           const int tok = 2 * c + (n & 1) + 8 * (n >> 1);
           const uint32_t s = v_scales[tok * (D / kGroup) + (j * 8 + r) * Sh::kVElems / kGroup];
-          f[n] = half_factor(tok < sp.len - t ? s : 0u, tok < sp.len - t ? v_top[n] : 0u);
+          f[n] = half_factor(tok < held ? s : 0u, __shfl_sync(~0u, top, tok));
         }
         f01 = f[0] | f[1] << 16, f23 = f[2] | f[3] << 16;
       }
@@ -506,35 +538,37 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
           for (int i = 0; i < 4; ++i) odd |= odd2<kHalf>(b[i][0]) || odd2<kHalf>(b[i][1]);
           odd = __any_sync(~0u, odd);
         }
-        if (!odd) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; i += 2) {
+          float (&sum)[NR][4] = o[(j * Sh::kVElems + e0 + i) / 2];
+          if (!odd) {
+            const uint32_t av[4] = {b[i][0], b[i + 1][0], b[i][1], b[i + 1][1]};
 #pragma unroll
-            for (int n = 0; n < Sh::kLimbs; ++n) mma<kHalf>(o[j * Sh::kVElems + e0 + i], pa[n], b[i][0], b[i][1]);
-        } else {
-          // An infinity or NaN among the drafted tokens' values: only the rows that see it may get it, so
-          // the products are summed one by one.  Token (cc, n) of row r, r + 8 is lane (r, cc)'s p[h][n]; its
-          // value in column 2c (+ 1) is lane (2c (+ 1), cc)'s.
+            for (int y = 0; y < Sh::kLimbs; ++y)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+              for (int n = 0; n < NR; ++n) mma<kHalf>(sum[n], av, pb[y][n]);
+          } else {
+            // An infinity or NaN among the drafted tokens' values: only the rows that see it may get it, so
+            // the products are summed one by one.  Token 2 cc + x + 8 h of column r is lane (r, cc)'s; its
+            // probabilities for rows 2c, 2c + 1 are lane (2 cc + x, c)'s.
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc)
+            for (int tok = 0; tok < kStep; ++tok) {
+              const int h = tok >> 3, node = t + tok - before;
+              const uint32_t u = __shfl_sync(~0u, h ? b[i][1] : b[i][0], 4 * r + (tok & 7) / 2),
+                             v = __shfl_sync(~0u, h ? b[i + 1][1] : b[i + 1][0], 4 * r + (tok & 7) / 2);
+              const float2 xu = unpack2<kHalf>(u), xv = unpack2<kHalf>(v);
 #pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                const int tok = 2 * cc + (n & 1) + 8 * (n >> 1), node = t + tok - before;
-                const uint32_t u = __shfl_sync(~0u, b[i][n >> 1], 8 * c + cc),
-                               v = __shfl_sync(~0u, b[i][n >> 1], 8 * c + 4 + cc);
-                const float2 x = unpack2<kHalf>(u), y = unpack2<kHalf>(v);
+              for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float pr = __shfl_sync(~0u, p[h][n], 4 * r + cc);
-                  const bool seen = node < 0 || (node < sp.rows && (word[h] >> node & 1));
-                  if (seen) {
-                    o[j * Sh::kVElems + e0 + i][2 * h] += pr * (n & 1 ? x.y : x.x);
-                    o[j * Sh::kVElems + e0 + i][2 * h + 1] += pr * (n & 1 ? y.y : y.x);
+                for (int x = 0; x < 2; ++x) {
+                  const float pr = __shfl_sync(~0u, h ? p[n][2 + x] : p[n][x], 4 * (tok & 7) + c);
+                  if (node < 0 || (node < sp.rows && (words[8 * n + 2 * c + x] >> node & 1))) {
+                    sum[n][x] += pr * (tok & 1 ? xu.y : xu.x);
+                    sum[n][2 + x] += pr * (tok & 1 ? xv.y : xv.x);
                   }
                 }
-              }
+            }
+          }
         }
       }
     }
@@ -542,73 +576,76 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
   copy_wait<0>();
 
   // ---- the warps' sums, to the rows' true maxima ----
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int x = 1; x <= 2; x *= 2) {
-      m_true[h] = fmaxf(m_true[h], __shfl_xor_sync(~0u, m_true[h], x));
-      l[h] += __shfl_xor_sync(~0u, l[h], x);
-    }
-  }
   __syncthreads();                                 // the ring is done: its place takes the sums
-  float* mine = reinterpret_cast<float*>(body) + warp * 16 * (D + 4);
+  float* mine = reinterpret_cast<float*>(body) + warp * Sh::kRows * (D + 4);
+  const float unit = Sh::kCoded ? scale_value(ref) : 1.f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float to = m_true[h] == -INFINITY ? 0.f : exp2f(m_ref[h] - m_true[h] - kBase);
-    const float unit = Sh::kCoded ? scale_value((uint32_t)ref) : 1.f;
-    if (c == 0) sums[warp * 16 + r + 8 * h] = make_float2(m_true[h], l[h] * to);
+  for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int j = 0; j < Sh::kVVecs; ++j)
+    for (int x = 0; x < 2; ++x) {
 #pragma unroll
-      for (int e = 0; e < Sh::kVElems; ++e)
+      for (int y = 4; y <= 16; y *= 2) {
+        m_true[n][x] = fmaxf(m_true[n][x], __shfl_xor_sync(~0u, m_true[n][x], y));
+        l[n][x] += __shfl_xor_sync(~0u, l[n][x], y);
+      }
+      const int row = 8 * n + 2 * c + x;
+      const float to = m_true[n][x] == -INFINITY ? 0.f : exp2f(m_ref[n][x] - m_true[n][x] - kBase);
+      if (r == 0) sums[warp * Sh::kRows + row] = make_float2(m_true[n][x], l[n][x] * (l[n][x] == l[n][x] ? to : 1.f));
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          mine[(r + 8 * h) * (D + 4) + (j * 8 + 2 * c + x) * Sh::kVElems + e] =
-              o[j * Sh::kVElems + e][2 * h + x] * to * unit;
-  }
+      for (int j = 0; j < Sh::kVVecs; ++j)
+#pragma unroll
+        for (int e = 0; e < Sh::kVElems; ++e)
+          mine[row * (D + 4) + (j * 8 + r) * Sh::kVElems + e] =
+              o[(j * Sh::kVElems + e) / 2][n][e % 2 * 2 + x] * to * unit;
+    }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * (D / 4); i += kWarps * 32) {
+  for (int i = threadIdx.x; i < Sh::kRows * (D / 4); i += kWarps * 32) {
     const int lr = i / (D / 4), d = i % (D / 4) * 4, row = row0 + lr;
     if (row >= M) break;
     float m = -INFINITY, lsum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sums[w * 16 + lr].x);
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sums[w * Sh::kRows + lr].x);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 s = sums[w * 16 + lr];
+      const float2 s = sums[w * Sh::kRows + lr];
       const float f = exp2f(s.x - (m == -INFINITY ? 0.f : m));
-      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(body) + (w * 16 + lr) * (D + 4) + d);
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(body) + (w * Sh::kRows + lr) * (D + 4) + d);
       lsum += s.y * f;
       v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
     }
-    const long long at = (long long)(sp.first + row / G) * a.q_heads + head * G + row % G;
     if (parts.count == 1) {
-      finish4<F32>(a, at, d, v, m, lsum);
+      finish4<F32>(a, (long long)(sp.first + row / G) * a.q_heads + head * G + row % G, d, v, m, lsum);
     } else {
-      const long long to = ((long long)part * gridDim.z * gridDim.y + seq * gridDim.y + blockIdx.y) * kTileRows + lr;
+      const long long to = ((long long)part * gridDim.z * gridDim.y + seq * gridDim.y + blockIdx.y) * Sh::kRows + lr;
       *reinterpret_cast<float4*>(parts.o + to * D + d) = v;
       if (d == 0) parts.ml[to] = make_float2(m, lsum);
     }
   }
 }
 
-template <int FMT, bool F32>
+template <int FMT, bool F32, int NR>
 cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
-  using Sh = Shape<FMT, F32>;
+  using Sh = Shape<FMT, F32, NR>;
   // the kernel's shared memory is set once for each device (twice by two threads at once does no harm)
   static std::atomic<unsigned long long> set{0};
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(set.load(std::memory_order_relaxed) & bit)) {
-    if (cudaError_t e = cudaFuncSetAttribute(parts_kernel<FMT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem))
+    if (cudaError_t e = cudaFuncSetAttribute(parts_kernel<FMT, F32, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem))
       return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int tiles = (a.max_rows * (a.q_heads / a.c.heads) + kTileRows - 1) / kTileRows;
-  parts_kernel<FMT, F32><<<dim3(p.count, a.c.heads * tiles, a.b.n_seqs), kWarps * 32, Sh::kSmem, st>>>(a, p);
+  parts_kernel<FMT, F32, NR><<<dim3(p.count, a.c.heads * p.tiles, a.b.n_seqs), kWarps * 32, Sh::kSmem, st>>>(a, p);
   return cudaGetLastError();
+}
+template <int FMT, bool F32>
+cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
+  if (p.tile_rows == 8) return launch<FMT, F32, 1>(a, p, st);
+  if (p.tile_rows == 16) return launch<FMT, F32, 2>(a, p, st);
+  if constexpr (D <= kWideDim) return launch<FMT, F32, 4>(a, p, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -13,17 +13,18 @@
 namespace tactkv {
 namespace text {
 
-constexpr int kTileRows = 16;      // rows (node, query head of the group) of a unit of work
-constexpr int kMaxParts = 2 * 148; // units times parts: two CTAs on each of the 148 SMs
-constexpr int kLeastPart = 128;    // tokens
+constexpr int kMaxParts = 4 * 148; // units times parts, where there is more than one part
+constexpr int kLeastPart = 256;    // tokens
+constexpr int kWideDim = 128;      // up to this head_dim a unit may have 32 rows (registers for their sums)
 
-// A unit is (sequence, K/V head, row tile), numbered in that order.  Units times parts is at most
-// kMaxParts when there is more than one part, so the workspace has one size.
+// A unit is (sequence, K/V head, tile of tile_rows rows), numbered in that order.
 struct Parts {
+  int tile_rows;       // 8, 16 or 32
+  int tiles;           // for max_rows * G rows
   int tokens;          // per part, a multiple of 64
   int count;           // parts of the longest sequence
-  float* o;            // [count][unit][kTileRows][D] sums of exp2(z - m) V
-  float2* ml;          // [count][unit][kTileRows] m (log2), l
+  float* o;            // [count][unit][tile_rows][D] sums of exp2(z - m) V
+  float2* ml;          // [count][unit][tile_rows] m (log2), l
 };
 
 constexpr float kLn2 = 0.69314718055994531f;

@@ -15,16 +15,16 @@ constexpr int kThreads = 128;
 
 // out, m and l of one (row, query head): its parts' sums, each to the largest maximum, in the parts' order.
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, const Parts p, int tiles) {
+__global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, const Parts p) {
   __shared__ float4 sum[kThreads];
   __shared__ float part_l[kThreads];
   const int D = a.c.head_dim, G = a.q_heads / a.c.heads;
-  const int unit = blockIdx.y, tile = unit % tiles, head = unit / tiles % a.c.heads, seq = unit / tiles / a.c.heads;
+  const int unit = blockIdx.y, tile = unit % p.tiles, head = unit / p.tiles % a.c.heads, seq = unit / p.tiles / a.c.heads;
   const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
-  const int row = tile * kTileRows + blockIdx.x;
+  const int row = tile * p.tile_rows + blockIdx.x;
   if (!sp.ok || row >= sp.rows * G) return;
   const int n = max(1, (sp.len + p.tokens - 1) / p.tokens);
-  const long long stride = (long long)gridDim.y * kTileRows, at = (long long)unit * kTileRows + blockIdx.x;
+  const long long stride = (long long)gridDim.y * p.tile_rows, at = (long long)unit * p.tile_rows + blockIdx.x;
   const int cols = D / 4, groups = kThreads / cols, g = threadIdx.x / cols, d = threadIdx.x % cols * 4;
   float m = -INFINITY;
   for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, p.ml[i * stride + at].x);
@@ -58,19 +58,21 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, con
 }  // namespace
 
 size_t attention_workspace(int head_dim) {
-  return (size_t)kMaxParts * kTileRows * (head_dim * sizeof(float) + sizeof(float2));
+  return (size_t)kMaxParts * (head_dim <= kWideDim ? 32 : 16) * (head_dim * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspace, cudaStream_t st) {
-  const int tiles = (a.max_rows * (a.q_heads / a.c.heads) + kTileRows - 1) / kTileRows;
-  const long long units = (long long)a.b.n_seqs * a.c.heads * tiles;
+  const int rows = a.max_rows * (a.q_heads / a.c.heads), wide = a.c.head_dim <= kWideDim ? 32 : 16;
   Parts p;
+  p.tile_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : wide);
+  p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+  const long long units = (long long)a.b.n_seqs * a.c.heads * p.tiles;
   const long long most = (a.max_len + kLeastPart - 1) / kLeastPart;
   p.count = (int)std::max(1ll, std::min(most, kMaxParts / units));
   p.tokens = std::max(kLeastPart, ((a.max_len + p.count - 1) / p.count + 63) / 64 * 64);
   p.count = std::max(1, (a.max_len + p.tokens - 1) / p.tokens);
   p.o = static_cast<float*>(workspace);
-  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kMaxParts * kTileRows * a.c.head_dim);
+  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kMaxParts * wide * a.c.head_dim);
   cudaError_t e = cudaErrorInvalidValue;
   switch (a.c.head_dim) {
 #define TACTKV_CASE(D) case D: e = launch_parts_##D(fmt, f32, a, p, st); break;
@@ -78,9 +80,9 @@ cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspa
 #undef TACTKV_CASE
   }
   if (e != cudaSuccess || p.count == 1) return e;
-  const dim3 grid(kTileRows, (unsigned)units);
-  if (f32) combine_kernel<true><<<grid, kThreads, 0, st>>>(a, p, tiles);
-  else combine_kernel<false><<<grid, kThreads, 0, st>>>(a, p, tiles);
+  const dim3 grid(p.tile_rows, (unsigned)units);
+  if (f32) combine_kernel<true><<<grid, kThreads, 0, st>>>(a, p);
+  else combine_kernel<false><<<grid, kThreads, 0, st>>>(a, p);
   return cudaGetLastError();
 }
 
