@@ -41,6 +41,7 @@ UNITS = [
     ("pack", "pack.cu", []),
     ("text_cache", "text_cache.cu", []),
     *[(f"text_attention_{d}", "text_attention.cu", [f"-DTACTKV_TEXT_D={d}"]) for d in range(32, 257, 32)],
+    *[(f"text_tc_{d}", "text_tc.cu", [f"-DTACTKV_TEXT_D={d}"]) for d in (64, 128, 192, 256)],
     ("text_parts", "text_parts.cu", []),
     ("text", "text.cu", []),
     ("tactkv", "tactkv.cu", []),

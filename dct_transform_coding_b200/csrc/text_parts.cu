@@ -1,4 +1,6 @@
 // Attention over the text cache: the launch plan, and the sum over a sequence's parts.
+#include <cstdlib>
+
 #include "text_attention.cuh"
 
 namespace tactkv {
@@ -7,6 +9,9 @@ namespace text {
 #define TACTKV_FOR_D(X) X(32) X(64) X(96) X(128) X(160) X(192) X(224) X(256)
 #define TACTKV_DECL(D) cudaError_t launch_parts_##D(int, bool, const AttnArgs&, const Parts&, cudaStream_t);
 TACTKV_FOR_D(TACTKV_DECL)
+#undef TACTKV_DECL
+#define TACTKV_DECL(D) cudaError_t launch_tc_##D(int, const AttnArgs&, const Parts&, cudaStream_t);
+TACTKV_DECL(64) TACTKV_DECL(128) TACTKV_DECL(192) TACTKV_DECL(256)
 #undef TACTKV_DECL
 
 namespace {
@@ -58,26 +63,34 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, con
 }  // namespace
 
 size_t attention_workspace(int head_dim) {
-  return (size_t)kMaxParts * (head_dim <= kWideDim ? 32 : 16) * (head_dim * sizeof(float) + sizeof(float2));
+  return (size_t)kMaxParts * kPartRows(head_dim) * (head_dim * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspace, cudaStream_t st) {
-  const int rows = a.max_rows * (a.q_heads / a.c.heads), wide = a.c.head_dim <= kWideDim ? 32 : 16;
+  const int D = a.c.head_dim, rows = a.max_rows * (a.q_heads / a.c.heads);
+  const bool tc = !f32 && D % 64 == 0 && !getenv("NOTC");
   Parts p;
-  p.tile_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : wide);
+  if (tc) p.tile_rows = rows <= 16 ? 16 : (rows <= 32 || D > kWideDim ? 32 : 64);
+  else p.tile_rows = rows <= 8 ? 8 : (rows <= 16 || D > kWideDim ? 16 : 32);
   p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   const long long units = (long long)a.b.n_seqs * a.c.heads * p.tiles;
-  const long long most = (a.max_len + kLeastPart - 1) / kLeastPart;
-  p.count = (int)std::max(1ll, std::min(most, kMaxParts / units));
-  p.tokens = std::max(kLeastPart, ((a.max_len + p.count - 1) / p.count + 63) / 64 * 64);
+  const int grain = 128;
+  int least = kLeastPart; if (getenv("LEAST")) least = atoi(getenv("LEAST"));
+  int mp = tc ? 148 : kMaxParts; if (getenv("MP")) mp = atoi(getenv("MP"));
+  const long long most = (a.max_len + least - 1) / least;
+  p.count = (int)std::max(1ll, std::min(most, mp / units));
+  p.tokens = std::max(least, ((a.max_len + p.count - 1) / p.count + grain - 1) / grain * grain);
   p.count = std::max(1, (a.max_len + p.tokens - 1) / p.tokens);
   p.o = static_cast<float*>(workspace);
-  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kMaxParts * wide * a.c.head_dim);
+  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kMaxParts * kPartRows(D) * D);
   cudaError_t e = cudaErrorInvalidValue;
-  switch (a.c.head_dim) {
+  switch (D) {
 #define TACTKV_CASE(D) case D: e = launch_parts_##D(fmt, f32, a, p, st); break;
-    TACTKV_FOR_D(TACTKV_CASE)
+#define TACTKV_CASE_TC(D) case D: e = tc ? launch_tc_##D(fmt, a, p, st) : launch_parts_##D(fmt, f32, a, p, st); break;
+    TACTKV_CASE(32) TACTKV_CASE_TC(64) TACTKV_CASE(96) TACTKV_CASE_TC(128) TACTKV_CASE(160) TACTKV_CASE_TC(192)
+    TACTKV_CASE(224) TACTKV_CASE_TC(256)
 #undef TACTKV_CASE
+#undef TACTKV_CASE_TC
   }
   if (e != cudaSuccess || p.count == 1) return e;
   const dim3 grid(p.tile_rows, (unsigned)units);
