@@ -130,6 +130,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
+constexpr uint32_t kIdescBMn = 1u << 16;   // B MN-major
 // The same with half-precision A and B.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn) {
   return idesc_bf16(M, N, a_mn) & ~((1u << 7) | (1u << 10));

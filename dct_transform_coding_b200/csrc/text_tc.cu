@@ -9,12 +9,14 @@
 //   softmax (4 or 8)  S^T from tensor memory -> P in shared memory; running maximum and sum in registers
 //   producer (1)      copies pages: TMA tiles into operand slots (bfloat16), bulk copies into raw slots (coded)
 //   issuer (1)        all products; the next tile's S^T is issued before this tile's O^T waits for its softmax
-//   decoders (8, 4)   coded caches: raw slots -> half-precision operands, once for all rows of the unit
+//   scaler (1)        coded caches: each token's largest scale, and its groups' distances to it
+//   decoders (8, 16)  coded caches: raw slots -> half-precision operands, once for all rows of the unit
 // Every wait is bounded; one that expires records TACTKV_TIMEOUT and ends the block's work.
 //
 // An infinity or NaN in the V of a drafted token must reach only the rows that see it, so it is taken out of
 // the operand, and its rows get it in plain arithmetic at the end.
 #include <atomic>
+#include <cfloat>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -32,8 +34,11 @@ namespace {
 
 constexpr int D = TACTKV_TEXT_D;
 constexpr int TT = 128;                           // tokens of a tile
+constexpr int kMaxSlots = 12;
+constexpr int R = 16;                             // rows of a softmax warpgroup
 constexpr float kToLog2 = to_log2(D);
-constexpr uint32_t kPolls = 1u << 20;             // of a wait; each may block for microseconds
+constexpr uint32_t kPolls = 1u << 16;             // of a wait; each suspends the thread for up to kPause ns
+constexpr uint32_t kPause = 20000;
 
 template <int FMT, int N>
 struct Shape {
@@ -42,32 +47,38 @@ struct Shape {
   static constexpr int kGroups = (D + 127) / 128; // of 128 output columns (the last may be half empty)
   static constexpr int kBlock = TT * 128;
   static constexpr int kOp = kBlocks * kBlock;
-  static constexpr int kWGs = N == 64 ? 2 : 1;
-  static constexpr int kRowsWG = N / kWGs;
-  static constexpr int kDecoders = !kCoded ? 0 : (N == 64 ? 4 : 8);
-  static constexpr int kThreads = 32 * (4 * kWGs + 2 + kDecoders);
+  static constexpr int kWGs = N / R;              // softmax warpgroups, R rows each
   static constexpr int kRow = D * code_bits(FMT) / 8;
-  static constexpr int kRaw = TT * kRow, kRawScales = TT * (D / kGroup);
+  static constexpr int kParts = kCoded ? 2 : 1, kPart = TT / kParts;            // a slot holds a half or all of K's or V's tile
+  static constexpr int kRaw = kPart * kRow, kRawScales = kPart * (D / kGroup);
   static constexpr int kSlot = kCoded ? kRaw + kRawScales : kOp;
-  static constexpr int kQ = kBlocks * N * 128, kP = 2 * N * 128;
-  static constexpr int kFactors = kCoded ? TT * (D / kGroup) * 2 : 0;           // of the tile being decoded
-  static constexpr int kTops = kCoded ? 4 * TT : 0;                            // [K, V][parity][token]
-  static constexpr int kMisc = 2048 + 24 * N + kWGs * 4 * 8 * kRowsWG;
+  static constexpr int kQ = kBlocks * N * 128, kP = TT * N * 2;
+  static constexpr int kFactors = kCoded ? 256 : 0;                            // 2^-i, twice in half precision
+  static constexpr int kTops = kCoded ? 8 * TT : 0;                            // [tile % 4][K, V][token]
+  static constexpr int kMisc = 1024 + 24 * N + kWGs * 4 * 8 * R;
   // With an odd number of blocks the last product reads a block past V's operand: something must be there.
   static constexpr int kPad = kBlocks % 2 ? kBlock : 0;
-  static constexpr int kFixed = 1024 + (kCoded ? 2 * kOp : 0) + kQ + kP + kFactors + kTops + kMisc + kPad;
-  static constexpr int kFit = (227 * 1024 - kFixed) / kSlot;
-  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = kFixed + kSlots * kSlot;
+  static constexpr int kRest = 1024 + kQ + kP + kFactors + kTops + kMisc + kPad;
+  // Two blocks on an SM where two slots fit each: one's start, end and waits are the other's time.
+  static constexpr int kCtas = N <= (kCoded ? 16 : 32) && kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot <= 113 * 1024 ? 2 : 1;
+  static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;        // V operands in turn
+  static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
+  static constexpr int kDecoders = !kCoded ? 0 : (N <= 32 && kCtas == 1 ? 16 : 8);
+  static constexpr int kThreads = 32 * (4 * kWGs + 2 + (kCoded ? 1 + kDecoders : 0));
+  static constexpr int kFit = ((kCtas == 2 ? 113 : 227) * 1024 - kRest - kOps) / kSlot;
+  static constexpr int kSlots = kFit > kMaxSlots ? kMaxSlots : kFit;
+  static constexpr int kSmem = kRest + kOps + kSlots * kSlot;
   static constexpr int kCols = (2 + kGroups) * N;
   static constexpr int kTmem = kCols <= 32 ? 32 : (kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256));
-  static_assert(kSlots >= 2 && kCols <= 256, "");
-  static_assert(N * (D + 4) * 4 <= kSlots * kSlot + (kCoded ? 2 * kOp : 0), "the sums take the operands' place");
+  static_assert(kSlots >= 2 * kParts && kCols <= 256, "");
+  static_assert(N * (D + 4) * 4 <= kOps + (kCoded ? 0 : kSlots * kSlot), "the sums take the operands' place");
 };
 
 struct Bars {
-  uint64_t slot_full[8], slot_free[8], op_full[2], op_free[2], s_full[2], p_full, pv_done, drain;
+  uint64_t slot_full[kMaxSlots], slot_scaled[kMaxSlots], slot_free[kMaxSlots], op_full[3], op_free[3], tops_full[4],
+      s_full[2], p_full, pv_done, drain;
 };
+static_assert(sizeof(Bars) <= 512, "");
 
 // False if the phase did not complete within kPolls, or if another wait of the block expired (dead, where given).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
@@ -75,12 +86,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   for (uint32_t i = 0; i < kPolls; ++i) {
     uint32_t done;
     asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
-        : "r"(a), "r"(parity)
+        : "r"(a), "r"(parity), "r"(kPause)
         : "memory");
     if (done) return true;
-    if (dead && (i & 255) == 255 && *dead) return false;
+    if (dead && (i & 15) == 15 && *dead) return false;
   }
   if (dead) *dead = 1;
   return false;
@@ -108,8 +119,8 @@ __device__ float value_at(const Cache& c, int kv, long long at, int d) {
   return unpack2<true>(h[0]).x * f;
 }
 
-// Sums (or maxima) over the warp of R values a lane: lane i < R gets the i-th (R = 16, 32).
-template <int HALF, int R, bool MAX>
+// Sums (or maxima) over the warp of R = 16 values a lane: lane i gets the (i % 16)-th.
+template <int HALF, bool MAX>
 __device__ __forceinline__ void reduce_step(float (&v)[R]) {
   const bool upper = threadIdx.x & HALF;
 #pragma unroll
@@ -117,30 +128,26 @@ __device__ __forceinline__ void reduce_step(float (&v)[R]) {
     const float mine = upper ? v[HALF + i] : v[i], other = __shfl_xor_sync(~0u, upper ? v[i] : v[HALF + i], HALF);
     v[i] = MAX ? fmaxf(mine, other) : mine + other;
   }
-  if constexpr (HALF > 1) reduce_step<HALF / 2, R, MAX>(v);
+  if constexpr (HALF > 1) reduce_step<HALF / 2, MAX>(v);
 }
-template <int R, bool MAX>
+template <bool MAX>
 __device__ __forceinline__ float reduce_rows(float (&v)[R]) {
-  reduce_step<R / 2, R, MAX>(v);
-  if constexpr (R == 16) {
-    const float other = __shfl_xor_sync(~0u, v[0], 16);
-    return MAX ? fmaxf(v[0], other) : v[0] + other;
-  }
-  return v[0];
+  reduce_step<R / 2, MAX>(v);
+  const float other = __shfl_xor_sync(~0u, v[0], 16);
+  return MAX ? fmaxf(v[0], other) : v[0] + other;
 }
 
 template <int FMT, int N>
-__global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     tc_kernel(const AttnArgs a, const Parts parts, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<FMT, N>;
   constexpr bool kCoded = Sh::kCoded;
-  constexpr int R = Sh::kRowsWG;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* k_op = smem;                                             // coded: the operands ..
   unsigned char* v_op = k_op + (kCoded ? Sh::kOp : 0);
-  unsigned char* q_op = v_op + (kCoded ? Sh::kOp : 0);
+  unsigned char* q_op = smem + Sh::kOps;
   unsigned char* p_op = q_op + Sh::kQ;
   unsigned char* slots = p_op + Sh::kP;                                   // .. and raw slots; bfloat16: operand slots
   unsigned char* factors = slots + Sh::kSlots * Sh::kSlot + Sh::kPad;
@@ -151,11 +158,11 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
   volatile int* dead = reinterpret_cast<volatile int*>(misc + 516);
   uint32_t* odd_nodes = reinterpret_cast<uint32_t*>(misc + 520);          // 2 words
   uint32_t* absent_of = reinterpret_cast<uint32_t*>(misc + 576);          // [tile % 16] 16-token blocks on bad pages
-  unsigned long long* words = reinterpret_cast<unsigned long long*>(misc + 2048);
-  float* row_factor = reinterpret_cast<float*>(words + N);
-  float* m_ref = row_factor + N;
-  float2* row_ml = reinterpret_cast<float2*>(m_ref + N);
-  float* exchange = reinterpret_cast<float*>(row_ml + N);                 // [WG][warp][2 R]
+  unsigned long long* words = reinterpret_cast<unsigned long long*>(misc + 1024);
+  float2* row_ml = reinterpret_cast<float2*>(words + N);
+  float* row_factor = reinterpret_cast<float*>(row_ml + N);
+  float* m_ref = row_factor + N;                                          // the rows' references
+  float* exchange = m_ref + N;                                            // [WG][warp][2 R]
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = a.q_heads / a.c.heads;
@@ -180,16 +187,20 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
   const int n_tiles = (min(sp.len - t0, parts.tokens) + TT - 1) / TT;
 
   // ---- set up: barriers, tensor memory, the queries' operand ----
+  if (kCoded && threadIdx.x < 64)
+    reinterpret_cast<uint32_t*>(factors)[threadIdx.x] = half_factor(threadIdx.x == 63 ? 255u : 128u - threadIdx.x, 128u) * 0x10001u;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
       tc::mbar_init(&bars->slot_full[i], 1);
+      tc::mbar_init(&bars->slot_scaled[i], 1);
       tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders : 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->tops_full[i], 1);
+    for (int i = 0; i < 3; ++i) {                  // K's operand, V's (one or two)
       tc::mbar_init(&bars->op_full[i], kCoded ? Sh::kDecoders : 1);
       tc::mbar_init(&bars->op_free[i], 1);
-      tc::mbar_init(&bars->s_full[i], 1);
     }
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&bars->s_full[i], 1);
     tc::mbar_init(&bars->p_full, 128 * Sh::kWGs);
     tc::mbar_init(&bars->pv_done, 1);
     tc::mbar_init(&bars->drain, 1);
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
     }
     if (lane == 0) {
       row_factor[n] = back;
-      m_ref[n] = -INFINITY;
+      m_ref[n] = -FLT_MAX;                         // every score is far above it
       words[n] = a.tree ? a.tree[sp.first + node] : (node >= 63 ? ~0ull : (2ull << node) - 1);
     }
   }
@@ -242,37 +253,40 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
 
   if (warp == 4 * Sh::kWGs) {
     // ------------------------------------------------------------------------------ producer ---
-    const int page_tokens = 1 << a.c.page_log2, run = min(page_tokens, TT), runs = TT / run;
+    const int page_tokens = 1 << a.c.page_log2, run = min(page_tokens, Sh::kPart), runs = TT / run, of_part = Sh::kPart / run;
     bool ok = true;
     int issued = 0;
     for (int i = 0; i < n_tiles && ok; ++i) {
-      const int t = t0 + i * TT + lane * run;
+      const int t = t0 + i * TT + lane * run;      // a lane copies a run of tokens, which never leaves its page
       const bool there = lane < runs && t < sp.len;
-      int page = there ? __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2)) : -1;
+      const int page = there ? __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2)) : -1;
       const bool good = there && page >= 0 && page < a.c.n_pages;
       if (there && !good) report(a.status);
       const uint32_t bad = __reduce_or_sync(~0u, there && !good ? ((1u << run / 16) - 1) << (lane * run / 16) : 0u);
-      const int copies = __popc(__ballot_sync(~0u, good));
+      const uint32_t copies = __ballot_sync(~0u, good);
       const long long at = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & (page_tokens - 1));
       if (lane == 0) absent_of[i & 15] = bad;
-      for (int kv = 0; kv < 2 && ok; ++kv) {
-        const int s = 2 * i + kv, slot = s % Sh::kSlots, round = s / Sh::kSlots;
+      for (int x = 0; x < 2 * Sh::kParts && ok; ++x) {
+        const int s = 2 * Sh::kParts * i + x, kv = x / Sh::kParts, half = x % Sh::kParts;
+        const int slot = s % Sh::kSlots, round = s / Sh::kSlots;
         if (round) ok = wait(&bars->slot_free[slot], (round - 1) & 1, dead);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        if (lane == 0) tc::mbar_expect_tx(&bars->slot_full[slot], copies * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
+        const int mine = __popc(copies >> (half * of_part) & ((2u << (of_part - 1)) - 1));
+        if (lane == 0) tc::mbar_expect_tx(&bars->slot_full[slot], mine * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
         issued = s + 1;
         __syncwarp();
-        if (good) {
+        if (good && lane / of_part == half) {
           unsigned char* to = slots + slot * Sh::kSlot;
+          const int in = lane % of_part * run;      // the run's place in the slot
           if constexpr (kCoded) {
-            tc::bulk_load(to + lane * run * Sh::kRow, a.c.pages[kv] + at * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
-            tc::bulk_load(to + Sh::kRaw + lane * run * (D / kGroup), a.c.scales[kv] + at * (D / kGroup), run * (D / kGroup),
+            tc::bulk_load(to + in * Sh::kRow, a.c.pages[kv] + at * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
+            tc::bulk_load(to + Sh::kRaw + in * (D / kGroup), a.c.scales[kv] + at * (D / kGroup), run * (D / kGroup),
                           &bars->slot_full[slot]);
           } else {
 #pragma unroll
             for (int b = 0; b < Sh::kBlocks; ++b)
-              tc::tma_load_2d(to + b * Sh::kBlock + lane * run * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)at);
+              tc::tma_load_2d(to + b * Sh::kBlock + in * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)at);
           }
         }
       }
@@ -284,42 +298,54 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
     // -------------------------------------------------------------------------------- issuer ---
     if (lane == 0) {
       constexpr uint32_t kIdS = kCoded ? tc::idesc_f16(128, N, false) : tc::idesc_bf16(128, N, false);
-      constexpr uint32_t kIdO = kCoded ? tc::idesc_f16(128, N, true) : tc::idesc_bf16(128, N, true);
+      constexpr uint32_t kIdO = (kCoded ? tc::idesc_f16(128, N, true) : tc::idesc_bf16(128, N, true)) | tc::kIdescBMn;
+      // P is MN-major: a token's N rows are 32, 64 or 128 bytes with the swizzle of that width
+      constexpr uint32_t kSwizzle = N == 16 ? 6 : (N == 32 ? 4 : 2);
       const uint32_t q_addr = tc::smem_u32(q_op), p_addr = tc::smem_u32(p_op);
-      auto operand = [&](int s) { return tc::smem_u32(kCoded ? (s & 1 ? v_op : k_op) : slots + s % Sh::kSlots * Sh::kSlot); };
-      auto full = [&](int s) {
-        return kCoded ? wait(&bars->op_full[s & 1], s / 2 & 1, dead)
-                      : wait(&bars->slot_full[s % Sh::kSlots], s / Sh::kSlots & 1, dead);
+      auto op = [&](int i, int kv) { return kv ? 1 + i % Sh::kVOps : 0; };
+      auto operand = [&](int i, int kv) {
+        return tc::smem_u32(kCoded ? k_op + op(i, kv) * Sh::kOp : slots + (2 * i + kv) % Sh::kSlots * Sh::kSlot);
       };
-      auto release = [&](int s) { tc::mma_commit(kCoded ? &bars->op_free[s & 1] : &bars->slot_free[s % Sh::kSlots]); };
+      auto full = [&](int i, int kv) {
+        return kCoded ? wait(&bars->op_full[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, dead)
+                      : wait(&bars->slot_full[(2 * i + kv) % Sh::kSlots], (2 * i + kv) / Sh::kSlots & 1, dead);
+      };
+      auto release = [&](int i, int kv) {
+        tc::mma_commit(kCoded ? &bars->op_free[op(i, kv)] : &bars->slot_free[(2 * i + kv) % Sh::kSlots]);
+      };
+      const uint64_t q_desc = tc::smem_desc(q_addr, 16, 1024, 2), p_desc = tc::smem_desc(p_addr, 16, 8 * N * 2, kSwizzle);
       auto scores = [&](int i) {
-        if (!full(2 * i)) return false;
+        if (!full(i, 0)) return false;
         tc::fence_after_sync();
-        const uint32_t k_addr = operand(2 * i);
+        const uint64_t k_desc = tc::smem_desc(operand(i, 0), 16, 1024, 2);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_bf16(tmem + (i & 1) * N, tc::smem_desc(k_addr + k / 4 * Sh::kBlock + k % 4 * 32, 16, 1024, 2),
-                       tc::smem_desc(q_addr + k / 4 * (N * 128) + k % 4 * 32, 16, 1024, 2), kIdS, k > 0);
-        release(2 * i);
+        for (int k = 0; k < D / 16; ++k)           // addresses in descriptors count 16 bytes
+          tc::mma_bf16(tmem + (i & 1) * N, k_desc + (k / 4 * Sh::kBlock + k % 4 * 32) / 16,
+                       q_desc + (k / 4 * (N * 128) + k % 4 * 32) / 16, kIdS, k > 0);
         tc::mma_commit(&bars->s_full[i & 1]);
+        release(i, 0);
         return true;
       };
+      // With V's operand in place early the next scores go first and are ready when this softmax is; with one
+      // operand that the decoders fill in turn, this tile's sums do, and the decoders go on with V's next.
+      constexpr bool kAhead = !kCoded || Sh::kVOps == 2;
       bool ok = scores(0);
       for (int i = 0; i < n_tiles && ok; ++i) {
-        if (i + 1 < n_tiles) ok = scores(i + 1);
-        if (ok) ok = full(2 * i + 1);
+        if (kAhead && i + 1 < n_tiles) ok = scores(i + 1);
+        if (ok) ok = full(i, 1);
         if (ok) ok = wait(&bars->p_full, i & 1, dead);
         if (!ok) break;
         tc::fence_after_sync();
-        const uint32_t v_addr = operand(2 * i + 1);
+        const uint64_t v_desc = tc::smem_desc(operand(i, 1), Sh::kBlock, 1024, 2);
 #pragma unroll
         for (int g = 0; g < Sh::kGroups; ++g)
 #pragma unroll
           for (int k = 0; k < TT / 16; ++k)
-            tc::mma_bf16(tmem + (2 + g) * N, tc::smem_desc(v_addr + 2 * g * Sh::kBlock + k * 2048, Sh::kBlock, 1024, 2),
-                         tc::smem_desc(p_addr + k / 4 * (N * 128) + k % 4 * 32, 16, 1024, 2), kIdO, i > 0 || k > 0);
-        release(2 * i + 1);
+            tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16, p_desc + k * (16 * N * 2) / 16,
+                         kIdO, i > 0 || k > 0);
         tc::mma_commit(&bars->pv_done);
+        release(i, 1);
+        if (!kAhead && i + 1 < n_tiles) ok = scores(i + 1);
       }
       if (!ok) {                                   // products in flight end before tensor memory is released
         tc::mma_commit(&bars->drain);
@@ -331,127 +357,137 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
     // ------------------------------------------------------------------------------- softmax ---
     const int wg = warp / 4, tid = threadIdx.x & 127, bar = 1 + wg, rows0 = wg * R;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);            // lane 32 * (warp % 4) in bits 16 ..
-    float l[R] = {}, m_true[R];
+    float l[R] = {}, high[R];                      // the thread's tokens' sum, and maximum less the reference
 #pragma unroll
-    for (int n = 0; n < R; ++n) m_true[n] = -INFINITY;
+    for (int n = 0; n < R; ++n) high[n] = -INFINITY;
     uint32_t ref = 0;
     bool ok = true;
     for (int i = 0; i < n_tiles; ++i) {
-      ok = __all_sync(~0u, wait(&bars->s_full[i & 1], i / 2 & 1, dead));
-      ok = !bar_or(bar, 128, !ok);
-      if (!ok) break;
+      ok = wait(&bars->s_full[i & 1], i / 2 & 1, dead);
+      if constexpr (kCoded) ok &= wait(&bars->tops_full[i & 3], i / 4 & 1, dead);
+      ok = __all_sync(~0u, ok);
       tc::fence_after_sync();
       const int t = t0 + i * TT + tid, node = t - before;
-      const bool absent = t >= sp.len || (absent_of[i & 15] >> (tid / 16) & 1);
+      const uint32_t bad = absent_of[i & 15];
+      const bool absent = t >= sp.len || (bad >> (tid / 16) & 1);
       const bool tail = t0 + (i + 1) * TT > before;
       uint32_t v_top = 0;
       float k_scale = 1.f;
       if constexpr (kCoded) {
-        k_scale = scale_value(tops[(i & 1) * TT + tid]);
+        k_scale = scale_value(tops[(i & 3) * 2 * TT + tid]);
+        v_top = tops[((i & 3) * 2 + 1) * TT + tid];
       }
-      float z[R];
-#pragma unroll
-      for (int c = 0; c < R; c += 16) {
-        float x[16];
-        tc::tmem_ld<16>(lanes + (i & 1) * N + rows0 + c, x);
+      float x[R];
+      auto scores = [&]() {                        // x: the scores less the reference
+        tc::tmem_ld<R>(lanes + (i & 1) * N + rows0, x);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int n = 0; n < 16; ++n) z[c + n] = x[n];
-      }
+        for (int n = 0; n < R; ++n) x[n] = fmaf(x[n], k_scale * row_factor[rows0 + n], -m_ref[rows0 + n]);
+        if (tail || bad) {
 #pragma unroll
-      for (int n = 0; n < R; ++n) {
-        z[n] *= k_scale * row_factor[rows0 + n];
-        if (absent) z[n] = -INFINITY;
-      }
-      if (tail && node >= 0 && !absent) {
-#pragma unroll
-        for (int n = 0; n < R; ++n)
-          if (!(words[rows0 + n] >> node & 1)) z[n] = -INFINITY;
-      }
-      if constexpr (kCoded) {                      // V's scales are known when its operand is
-        ok = wait(&bars->op_full[1], i & 1, dead);
-        v_top = tops[(2 + (i & 1)) * TT + tid];
-      }
-      bool over = v_top > ref;
-#pragma unroll
-      for (int n = 0; n < R; ++n) {
-        m_true[n] = fmaxf(m_true[n], z[n]);
-        over |= z[n] > m_ref[rows0 + n] + kSlack;
-      }
-      if (i) {   // O is whole, and P's place free
+          for (int n = 0; n < R; ++n)
+            if (absent || (node >= 0 && !(words[rows0 + n] >> node & 1))) x[n] = -INFINITY;
+        }
+      };
+      scores();
+      if (i) {                                     // O is whole, and P's place free
         ok &= wait(&bars->pv_done, (i - 1) & 1, dead);
         ok = __all_sync(~0u, ok);
         tc::fence_after_sync();
       }
-      if (bar_or(bar, 128, over || !ok)) {
+      float most = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < R; ++n) most = fmaxf(most, x[n]);
+      if (bar_or(bar, 128, most > kSlack || v_top > ref || !ok)) {
         if (bar_or(bar, 128, !ok)) break;
-        // move the references: the largest score of every row, the largest V scale
+        // move the references: of the rows with such a score, to the largest of this tile; of V's scales, to the largest
         float v[R];
 #pragma unroll
-        for (int n = 0; n < R; ++n) v[n] = z[n];
-        const float high = reduce_rows<R, true>(v);
+        for (int n = 0; n < R; ++n) v[n] = x[n];
+        const float up = reduce_rows<true>(v);
         float* mine = exchange + (wg * 4 + (warp & 3)) * 2 * R;
-        if (lane < R) mine[lane] = high;
+        if (lane < R) mine[lane] = up;
         const uint32_t top = __reduce_max_sync(~0u, v_top);
         if (lane == 0) mine[R] = __uint_as_float(top);
         bar_sync(bar);
-        float keep = 1.f;                          // of row rows0 + tid
         uint32_t new_ref = ref;
 #pragma unroll
         for (int w = 0; w < 4; ++w) new_ref = max(new_ref, __float_as_uint(exchange[(wg * 4 + w) * 2 * R + R]));
+        float keep = 1.f;                          // of row rows0 + tid
         if (tid < R) {
-          float most = -INFINITY;
+          float by = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) most = fmaxf(most, exchange[(wg * 4 + w) * 2 * R + tid]);
-          const float old = m_ref[rows0 + tid];
-          if (most > old + kSlack) {
-            m_ref[rows0 + tid] = most;
-            keep = exp2_fast(old - most);
+          for (int w = 0; w < 4; ++w) by = fmaxf(by, exchange[(wg * 4 + w) * 2 * R + tid]);
+          if (by > kSlack) {
+            const float old = m_ref[rows0 + tid], next = old == -FLT_MAX ? -INFINITY : old + by;
+            m_ref[rows0 + tid] = next;
+            keep = old == -FLT_MAX ? 0.f : exp2_fast(old - next);
           }
         }
         bar_sync(bar);                             // the exchanged maxima are read
         if (tid < R) exchange[wg * 4 * 2 * R + tid] = keep;
         bar_sync(bar);
+        const float* keeps = exchange + wg * 4 * 2 * R;
+        // A row's first reference: the scores less -FLT_MAX have lost their digits, so the maximum is taken again.
+        bool first = false;
+#pragma unroll
+        for (int n = 0; n < R; ++n) first |= m_ref[rows0 + n] == -INFINITY;
+        if (first) {
+          tc::tmem_ld<R>(lanes + (i & 1) * N + rows0, v);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int n = 0; n < R; ++n) {
+            v[n] *= k_scale * row_factor[rows0 + n];
+            if (absent || (node >= 0 && !(words[rows0 + n] >> node & 1))) v[n] = -INFINITY;
+          }
+          const float z = reduce_rows<true>(v);
+          if (lane < R) exchange[(wg * 4 + (warp & 3)) * 2 * R + R + lane] = z;
+          bar_sync(bar);
+          if (tid < R && m_ref[rows0 + tid] == -INFINITY) {
+            float by = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) by = fmaxf(by, exchange[(wg * 4 + w) * 2 * R + R + tid]);
+            m_ref[rows0 + tid] = by;
+          }
+          bar_sync(bar);
+        }
         const float down = kCoded ? __uint_as_float((uint32_t)max(127 + (int)ref - (int)new_ref, 0) << 23) : 1.f;
         ref = new_ref;
-        const float* keeps = exchange + wg * 4 * 2 * R;
 #pragma unroll
-        for (int n = 0; n < R; ++n) l[n] *= keeps[n];
+        for (int n = 0; n < R; ++n) {
+          if (keeps[n] != 1.f) high[n] = -INFINITY;   // all before is below this tile's largest
+          l[n] *= keeps[n];
+        }
         if (i) {
 #pragma unroll
-          for (int g = 0; g < Sh::kGroups; ++g)
+          for (int g = 0; g < Sh::kGroups; ++g) {
+            const uint32_t at = lanes + (2 + g) * N + rows0;
+            tc::tmem_ld<R>(at, v);
+            tc::tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < R; c += 16) {
-              float o[16];
-              const uint32_t at = lanes + (2 + g) * N + rows0 + c;
-              tc::tmem_ld<16>(at, o);
-              tc::tmem_ld_wait();
-#pragma unroll
-              for (int n = 0; n < 16; ++n) o[n] *= keeps[c + n] * down;
-              tc::tmem_st16(at, o);
-            }
+            for (int n = 0; n < R; ++n) v[n] *= keeps[n] * down;
+            tc::tmem_st16(at, v);
+          }
           tc::tmem_st_wait();
         }
+        scores();
         bar_sync(bar);                             // before the factors' place is written again
       }
-      const float fold = kCoded ? __uint_as_float((uint32_t)max(127 + (int)v_top - (int)ref, 0) << 23) : 1.f;
-      unsigned char* p_at = p_op + tid / 64 * (N * 128) + tid % 8 * 2;
-      const int chunk = tid % 64 / 8;
+      const float fold = kCoded ? __uint_as_float((uint32_t)max(127 + (int)kBase + (int)v_top - (int)ref, 0) << 23) : 1.f;
+      uint32_t w[R / 2];
 #pragma unroll
-      for (int n = 0; n < R; ++n) {
-        const float r = m_ref[rows0 + n];
-        const float p = exp2_fast(z[n] + (kBase - (r == -INFINITY ? 0.f : r)));
-        l[n] += p;
-        unsigned short h;
-        if constexpr (kCoded) {
-          const __half x = __float2half_rn(p * fold);
-          h = *reinterpret_cast<const unsigned short*>(&x);
-        } else {
-          const __nv_bfloat16 x = __float2bfloat16_rn(p);
-          h = *reinterpret_cast<const unsigned short*>(&x);
-        }
-        *reinterpret_cast<unsigned short*>(p_at + (rows0 + n) * 128 + ((chunk ^ (n & 7)) << 4)) = h;
+      for (int n = 0; n < R; n += 2) {
+        const float p0 = exp2_fast(x[n]), p1 = exp2_fast(x[n + 1]);
+        high[n] = fmaxf(high[n], x[n]), high[n + 1] = fmaxf(high[n + 1], x[n + 1]);
+        l[n] += p0, l[n + 1] += p1;
+        w[n / 2] = pack2<kCoded>(kCoded ? p0 * fold : p0, kCoded ? p1 * fold : p1);
       }
+      // the token's rows, 16 bytes at a time; the swizzle xors their place with the address's bits 7 ..
+      unsigned char* p_at = p_op + tid * (N * 2);
+      const int turn = N == 16 ? tid >> 2 & 1 : (N == 32 ? tid >> 1 & 3 : tid & 7);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        *reinterpret_cast<uint4*>(p_at + (((rows0 / 8 + y) ^ turn) << 4)) = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
       if (!kCoded && tail && wg == 0) {
         // Behind the last token V's operand holds whatever the page holds (decoders write zeros there), and
         // a drafted token's infinities and NaN are for some rows only: zeros take their place.
@@ -459,7 +495,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
       }
       if (wg == 0 && ok && (absent ? !kCoded : tail && node >= 0)) {
         if (!tail && !kCoded) ok = wait(&bars->slot_full[(2 * i + 1) % Sh::kSlots], (2 * i + 1) / Sh::kSlots & 1, dead);
-        unsigned char* v = kCoded ? v_op : slots + (2 * i + 1) % Sh::kSlots * Sh::kSlot;
+        unsigned char* v = kCoded ? v_op + i % Sh::kVOps * Sh::kOp : slots + (2 * i + 1) % Sh::kSlots * Sh::kSlot;
+        if constexpr (kCoded) ok = wait(&bars->op_full[1 + i % Sh::kVOps], i / Sh::kVOps & 1, dead);
         bool odd = false;
         for (int b = 0; b < Sh::kBlocks; ++b)
           for (int x = 0; x < 8; ++x) {
@@ -487,15 +524,15 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
       tc::mbar_arrive(&bars->p_full);
     }
     if (ok) ok = wait(&bars->pv_done, (n_tiles - 1) & 1, dead);
-    if (bar_or(3, 128 * Sh::kWGs, !ok || *dead)) {
+    if (bar_or(5, 128 * Sh::kWGs, !ok || *dead)) {
       if (tid == 0) atomicCAS(a.status, 0u, (unsigned int)TACTKV_TIMEOUT);
     } else {
       // ---- the rows' true maxima and sums ----
       tc::fence_after_sync();
-      const float high = reduce_rows<R, true>(m_true);
-      const float total = reduce_rows<R, false>(l);
+      const float above = reduce_rows<true>(high);
+      const float total = reduce_rows<false>(l);
       if (lane < R) {
-        exchange[(wg * 4 + (warp & 3)) * 2 * R + lane] = high;
+        exchange[(wg * 4 + (warp & 3)) * 2 * R + lane] = above;
         exchange[(wg * 4 + (warp & 3)) * 2 * R + R + lane] = total;
       }
       bar_sync(bar);
@@ -506,28 +543,23 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
           m = fmaxf(m, exchange[(wg * 4 + w) * 2 * R + tid]);
           sum += exchange[(wg * 4 + w) * 2 * R + R + tid];
         }
-        const float to = m == -INFINITY ? 0.f : exp2f(m_ref[rows0 + tid] - m - kBase);
-        row_ml[rows0 + tid] = make_float2(m, sum * to);
-        row_factor[rows0 + tid] = to * (kCoded ? scale_value(ref) : 1.f);   // of the row's sums
+        const float to = m == -INFINITY ? 0.f : exp2f(-m);
+        row_ml[rows0 + tid] = make_float2(m == -INFINITY ? m : m_ref[rows0 + tid] + m, sum * to);
+        row_factor[rows0 + tid] = to * (kCoded ? scale_value(ref) * 0.015625f : 1.f);   // of the row's sums
       }
       bar_sync(bar);
-      float* sums = reinterpret_cast<float*>(smem) + 0;
-      if constexpr (!kCoded) sums = reinterpret_cast<float*>(slots);
+      float* sums = reinterpret_cast<float*>(kCoded ? smem : slots);
 #pragma unroll
-      for (int g = 0; g < Sh::kGroups; ++g)
+      for (int g = 0; g < Sh::kGroups; ++g) {
+        float o[R];
+        tc::tmem_ld<R>(lanes + (2 + g) * N + rows0, o);
+        tc::tmem_ld_wait();
+        if (g * 128 + tid < D) {
 #pragma unroll
-        for (int c = 0; c < R; c += 16) {
-          float o[16];
-          tc::tmem_ld<16>(lanes + (2 + g) * N + rows0 + c, o);
-          tc::tmem_ld_wait();
-          if (g * 128 + tid < D) {
-#pragma unroll
-            for (int n = 0; n < 16; ++n)
-              sums[(rows0 + c + n) * (D + 4) + g * 128 + tid] = o[n] * row_factor[rows0 + c + n];
-          }
+          for (int n = 0; n < R; ++n) sums[(rows0 + n) * (D + 4) + g * 128 + tid] = o[n] * row_factor[rows0 + n];
         }
+      }
       // Infinities and NaN of drafted tokens, for the rows that see them (rare): p by one thread a row.
-      if (Sh::kWGs > 1) asm volatile("bar.sync 3, %0;\n" ::"n"(128 * Sh::kWGs) : "memory");   // both have added theirs
       for (int j = 0; j < sp.rows; ++j) {
         if (!(odd_nodes[j >> 5] >> (j & 31) & 1)) continue;
         const int t = before + j;
@@ -572,69 +604,121 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, 1)
       }
     }
     tc::fence_before_sync();
-  } else if constexpr (kCoded) {
-    // ------------------------------------------------------------------------------ decoders ---
-    constexpr int kTokens = TT / Sh::kDecoders;                            // a warp's tokens of every tile
-    constexpr int kPer = 16 * 8 / code_bits(FMT), kPieces = D / kPer;       // values in 16 bytes, pieces of a row
-    const int dw = warp - 4 * Sh::kWGs - 2, first = dw * kTokens;
-    constexpr int kGroupsRow = D / kGroup;
-    bool ok = true;
-    for (int s = 0; s < 2 * n_tiles && ok; ++s) {
-      const int i = s / 2, kv = s & 1, slot = s % Sh::kSlots;
-      ok = wait(&bars->slot_full[slot], s / Sh::kSlots & 1, dead);
-      if (ok && i) ok = wait(&bars->op_free[kv], (i - 1) & 1, dead);
-      ok = __all_sync(~0u, ok);
-      if (!ok) break;
-      const unsigned char* raw = slots + slot * Sh::kSlot;
-      const int held = sp.len - (t0 + i * TT);
-      const uint32_t bad = absent_of[i & 15];
-      // a lane takes one token's scales: the largest (the NaN scale aside), and every group's factor to it
-      if (lane < kTokens) {
-        const int tok = first + lane;
-        const bool absent = tok >= held || (bad >> (tok / 16) & 1);
-        const unsigned char* sc = raw + Sh::kRaw + tok * kGroupsRow;
-        uint32_t b[kGroupsRow], top = 0;
+  } else if (kCoded && warp == 4 * Sh::kWGs + 2) {
+    // -------------------------------------------------------------------------------- scaler ---
+    // A lane takes a token: the largest of its scales (the NaN scale aside), and in the scales' place every
+    // group's distance to it (31: 2^-25 and less are 0 in half precision; 63: NaN).
+    if constexpr (kCoded) {
+      constexpr int kGroupsRow = D / kGroup;
+      bool ok = true;
+      for (int s = 0; s < 4 * n_tiles && ok; ++s) {
+        const int i = s / 4, kv = s / 2 & 1, half = s & 1, slot = s % Sh::kSlots;
+        ok = __all_sync(~0u, wait(&bars->slot_full[slot], s / Sh::kSlots & 1, dead));
+        if (!ok) break;
+        const int held = sp.len - (t0 + i * TT);
+        const uint32_t bad = absent_of[i & 15];
 #pragma unroll
-        for (int g = 0; g < kGroupsRow; ++g) {
-          b[g] = sc[g];
-          top = max(top, b[g] == 255u ? 0u : b[g]);
-        }
-        if (absent) top = 0;
-        tops[(2 * kv + (i & 1)) * TT + tok] = (unsigned char)top;
+        for (int x = 0; x < Sh::kPart / 32; ++x) {
+          const int in = 32 * x + lane, tok = half * Sh::kPart + in;
+          const bool absent = tok >= held || (bad >> (tok / 16) & 1);
+          unsigned char* sc = slots + slot * Sh::kSlot + Sh::kRaw + in * kGroupsRow;
+          uint32_t b[kGroupsRow], top = 0;
+          if constexpr (kGroupsRow % 4 == 0) {
 #pragma unroll
-        for (int g = 0; g < kGroupsRow; ++g)
-          reinterpret_cast<unsigned short*>(factors)[tok * kGroupsRow + g] = absent ? 0 : (unsigned short)half_factor(b[g], top);
-      }
-      __syncwarp();
-      unsigned char* op = kv ? v_op : k_op;
-#pragma unroll 2
-      for (int x = lane; x < kTokens * kPieces; x += 32) {
-        const int tok = first + x / kPieces, piece = x % kPieces, d = piece * kPer;
-        uint4 w = *reinterpret_cast<const uint4*>(raw + tok * Sh::kRow + piece * 16);
-        if (tok >= held || (bad >> (tok / 16) & 1)) w = make_uint4(0, 0, 0, 0);
-        const uint32_t f = reinterpret_cast<const unsigned short*>(factors)[tok * kGroupsRow + d / kGroup] * 0x10001u;
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-        uint32_t h[kPer / 2];
+            for (int g = 0; g < kGroupsRow; g += 4) {
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + g);
+              b[g] = w & 255u, b[g + 1] = w >> 8 & 255u, b[g + 2] = w >> 16 & 255u, b[g + 3] = w >> 24;
+            }
+          } else {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          if constexpr (FMT == kFp8) unpack_e4m3x4(in[y], h[2 * y], h[2 * y + 1]);
-          else {
-            uint32_t u[4];
-            unpack_e2m1x8(in[y], u);
+            for (int g = 0; g < kGroupsRow; ++g) b[g] = sc[g];
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[4 * y + e] = u[e];
+          for (int g = 0; g < kGroupsRow; ++g) top = max(top, b[g] == 255u ? 0u : b[g]);
+          if (absent) top = 0;
+          tops[((i & 3) * 2 + kv) * TT + tok] = (unsigned char)top;
+#pragma unroll
+          for (int g = 0; g < kGroupsRow; ++g) b[g] = absent ? 0u : (b[g] == 255u ? 63u : min(top - min(b[g], top), 31u));
+          if constexpr (kGroupsRow % 4 == 0) {
+#pragma unroll
+            for (int g = 0; g < kGroupsRow; g += 4)
+              *reinterpret_cast<uint32_t*>(sc + g) = b[g] | b[g + 1] << 8 | b[g + 2] << 16 | b[g + 3] << 24;
+          } else {
+#pragma unroll
+            for (int g = 0; g < kGroupsRow; ++g) sc[g] = (unsigned char)b[g];
           }
         }
-        unsigned char* to = op + d / 64 * Sh::kBlock + tok * 128;
+        tc::fence_proxy_async();                   // the next copy into the slot comes after these stores
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&bars->slot_scaled[slot]);
+          if (kv && half) tc::mbar_arrive(&bars->tops_full[i & 3]);
+        }
+      }
+    }
+  } else if constexpr (kCoded) {
+    // ------------------------------------------------------------------------------ decoders ---
+    // A lane takes a group of 32 values at a time.  Eight lanes take four tokens' two groups of a 64-column block, and
+    // odd tokens their halves in the other order, so that stores of 16 bytes never meet in a bank.
+    constexpr int kAll = 32 * Sh::kDecoders, kGroupsRow = D / kGroup;
+    constexpr int kItems = Sh::kPart / 4 * Sh::kBlocks;                    // of eight lanes, in a slot
+    constexpr int kPasses = (kItems + kAll / 8 - 1) / (kAll / 8);
+    const int me = threadIdx.x - 32 * (4 * Sh::kWGs + 3);
+    bool ok = true;
+    for (int s = 0; s < 4 * n_tiles && ok; ++s) {
+      const int i = s / 4, kv = s / 2 & 1, half = s & 1, slot = s % Sh::kSlots;
+      const int op = kv ? 1 + i % Sh::kVOps : 0, turn = kv ? i / Sh::kVOps : i;
+      ok = wait(&bars->slot_scaled[slot], s / Sh::kSlots & 1, dead);
+      if (!half && turn) ok &= wait(&bars->op_free[op], (turn - 1) & 1, dead);
+      ok = __all_sync(~0u, ok);
+      if (!ok) break;
+      const int held = sp.len - (t0 + i * TT + half * Sh::kPart);
+      const uint32_t bad = absent_of[i & 15] >> (half * (Sh::kPart / 16));
+      const bool whole = held >= Sh::kPart && !(bad & ((1u << Sh::kPart / 16) - 1));
+      const unsigned char* raw = slots + slot * Sh::kSlot;
+      unsigned char* out = k_op + op * Sh::kOp + half * Sh::kPart * 128;
 #pragma unroll
-        for (int y = 0; y < kPer / 8; ++y)
-          *reinterpret_cast<uint4*>(to + ((d % 64 / 8 + y) ^ (tok & 7)) * 16) =
-              make_uint4(mul_half2(h[4 * y], f), mul_half2(h[4 * y + 1], f), mul_half2(h[4 * y + 2], f), mul_half2(h[4 * y + 3], f));
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int item = me / 8 + pass * (kAll / 8);
+        if (kItems % (kAll / 8) && item >= kItems) break;
+        const int block = item % Sh::kBlocks, tok = item / Sh::kBlocks * 4 + me % 8 / 2, g = block * 2 + me % 2;
+        const uint32_t f = reinterpret_cast<const uint32_t*>(factors)[raw[Sh::kRaw + tok * kGroupsRow + g]];
+        const bool absent = !whole && (tok >= held || (bad >> (tok / 16) & 1));
+        unsigned char* to = out + block * Sh::kBlock + tok * 128;
+        const int chunk = me % 2 * 4;
+        if constexpr (FMT == kFp8) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int part = y ^ (tok & 1);
+            uint4 w = *reinterpret_cast<const uint4*>(raw + tok * Sh::kRow + g * 32 + part * 16);
+            if (absent) w = make_uint4(0, 0, 0, 0);
+            uint32_t h[8];
+            unpack_e4m3x4(w.x, h[0], h[1]);
+            unpack_e4m3x4(w.y, h[2], h[3]);
+            unpack_e4m3x4(w.z, h[4], h[5]);
+            unpack_e4m3x4(w.w, h[6], h[7]);
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              *reinterpret_cast<uint4*>(to + ((chunk + part * 2 + z) ^ (tok & 7)) * 16) =
+                  make_uint4(mul_half2(h[4 * z], f), mul_half2(h[4 * z + 1], f), mul_half2(h[4 * z + 2], f), mul_half2(h[4 * z + 3], f));
+          }
+        } else {
+          uint4 w = *reinterpret_cast<const uint4*>(raw + tok * Sh::kRow + g * 16);
+          if (absent) w = make_uint4(0, 0, 0, 0);
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            uint32_t h[4];
+            unpack_e2m1x8(in[z], h);
+            *reinterpret_cast<uint4*>(to + ((chunk + z) ^ (tok & 7)) * 16) =
+                make_uint4(mul_half2(h[0], f), mul_half2(h[1], f), mul_half2(h[2], f), mul_half2(h[3], f));
+          }
+        }
       }
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(&bars->op_full[kv]);
+        if (half) tc::mbar_arrive(&bars->op_full[op]);
         tc::mbar_arrive(&bars->slot_free[slot]);
       }
     }
