@@ -127,15 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
   const int head = blockIdx.y / tiles, tile = blockIdx.y % tiles;
   const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
   if (!sp.ok) {                                   // the sequence's rows see no text token
-    if (part == 0 && tile == 0) {
-      if (threadIdx.x == 0) report(a.status);
-      const int end = __ldg(a.b.row_starts + seq + 1);
-      if (sp.first < 0 || end > a.b.n_rows) return;
-      for (int row = sp.first; row < end; ++row)
-        for (int i = threadIdx.x; i < G * (D / 4); i += kWarps * 32)
-          finish4<F32>(a, (long long)row * a.q_heads + head * G + i / (D / 4), i % (D / 4) * 4,
-                       make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
-    }
+    if (part == 0 && tile == 0) finish_misfit<F32, D>(a, sp, seq, head, G);
     return;
   }
   const int M = sp.rows * G, row0 = tile * Sh::kRows, before = sp.len - sp.rows;

@@ -87,31 +87,54 @@ __device__ __forceinline__ bool odd2(uint32_t v) {
 
 constexpr float kLn2 = 0.69314718055994531f;
 
-// out, m, l of (row, head) number `at` from the text tokens' sum o of columns d .. d+3, their maximum m2 (log2)
-// and l, merged with the prior.  A row that sees nothing has l = 0: out = 0, m = -inf.
-template <bool F32>
-__device__ __forceinline__ void finish4(const AttnArgs& a, long long at, int d, float4 o, float m2, float l) {
-  const int D = a.c.head_dim;
-  float m = l == l ? m2 * kLn2 : l;
+// A row's end: out = a * (the text tokens' sum) + b * prior_out.
+struct RowEnd {
+  float a, b;
+};
+// Of (row, head) number `at`, from the text tokens' maximum m2 (log2) and l, merged with the prior; write: m and l, too.
+// A row that sees nothing has l = 0: out = 0, m = -inf.
+__device__ __forceinline__ RowEnd end_row(const AttnArgs& a, long long at, float m2, float l, bool write) {
+  float m = l == l ? m2 * kLn2 : l, x = 1.f, y = 0.f;
   if (a.prior_out) {
     const float pm = a.prior_m[at], pl = a.prior_l[at];
-    const float4 p = *reinterpret_cast<const float4*>(a.prior_out + at * D + d);
     const float top = fmaxf(m, pm), safe = top == -INFINITY ? 0.f : top;
-    const float x = expf(m - safe), y = expf(pm - safe) * pl;
-    o.x *= x, o.y *= x, o.z *= x, o.w *= x;
-    if (pl != 0.f) o.x += p.x * y, o.y += p.y * y, o.z += p.z * y, o.w += p.w * y;
+    x = expf(m - safe), y = expf(pm - safe) * pl;
     l = l * x + y;
     m = l == l ? top : l;
   }
-  const float f = l == 0.f ? 0.f : 1.f / l;
-  if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if constexpr (F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + d) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-  } else {
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * D + d) =
-        make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+  if (write) a.m[at] = m, a.l[at] = l;
+  return l == 0.f ? RowEnd{0.f, 0.f} : RowEnd{x / l, y == 0.f ? 0.f : y / l};   // b = 0 without a prior, l a NaN or not
+}
+// Columns d .. d+3 of a row with the sum o.
+template <bool F32>
+__device__ __forceinline__ void finish4(const AttnArgs& a, long long at, int d, float4 o, RowEnd e) {
+  const int D = a.c.head_dim;
+  o.x *= e.a, o.y *= e.a, o.z *= e.a, o.w *= e.a;
+  if (e.b != 0.f) {   // what a prior of weight 0 holds does not matter
+    const float4 p = *reinterpret_cast<const float4*>(a.prior_out + at * D + d);
+    o.x += p.x * e.b, o.y += p.y * e.b, o.z += p.z * e.b, o.w += p.w * e.b;
   }
-  if (d == 0) a.m[at] = m, a.l[at] = l;
+  if constexpr (F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + d) = o;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * D + d) =
+        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
+template <bool F32>
+__device__ __forceinline__ void finish4(const AttnArgs& a, long long at, int d, float4 o, float m2, float l) {
+  finish4<F32>(a, at, d, o, end_row(a, at, m2, l, d == 0));
+}
+
+// The rows of a sequence whose numbers do not fit together see no text token.
+template <bool F32, int D>
+__device__ __forceinline__ void finish_misfit(const AttnArgs& a, const Span& sp, int seq, int head, int G) {
+  if (threadIdx.x == 0) report(a.status);
+  const int end = __ldg(a.b.row_starts + seq + 1);
+  if (sp.first < 0 || end > a.b.n_rows) return;
+  for (int row = sp.first; row < end; ++row)
+    for (int i = threadIdx.x; i < G * (D / 4); i += blockDim.x)
+      finish4<F32>(a, (long long)row * a.q_heads + head * G + i / (D / 4), i % (D / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f),
+                   -INFINITY, 0.f);
 }
 
 }  // namespace text

@@ -119,6 +119,18 @@ __device__ float value_at(const Cache& c, int kv, long long at, int d) {
   return unpack2<true>(h[0]).x * f;
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// Not zero if any of 16 half-precision values is an infinity or NaN (its exponent's carry).
+__device__ __forceinline__ uint32_t odd8(const uint32_t (&h)[8]) {
+  uint32_t y = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y |= (h[i] & 0x7C007C00u) + 0x04000400u;
+  return y & 0x80008000u;
+}
 // Sums (or maxima) over the warp of R = 16 values a lane: lane i gets the (i % 16)-th.
 template <int HALF, bool MAX>
 __device__ __forceinline__ void reduce_step(float (&v)[R]) {
@@ -157,12 +169,12 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 512);
   volatile int* dead = reinterpret_cast<volatile int*>(misc + 516);
   uint32_t* odd_nodes = reinterpret_cast<uint32_t*>(misc + 520);          // 2 words
+  uint32_t* odd_tile = reinterpret_cast<uint32_t*>(misc + 528);           // decoders met an infinity or NaN in a drafted V
   uint32_t* absent_of = reinterpret_cast<uint32_t*>(misc + 576);          // [tile % 16] 16-token blocks on bad pages
   unsigned long long* words = reinterpret_cast<unsigned long long*>(misc + 1024);
   float2* row_ml = reinterpret_cast<float2*>(words + N);
-  float* row_factor = reinterpret_cast<float*>(row_ml + N);
-  float* m_ref = row_factor + N;                                          // the rows' references
-  float* exchange = m_ref + N;                                            // [WG][warp][2 R]
+  float2* row_fm = row_ml + N;                                            // a row's factor, its reference's negative
+  float* exchange = reinterpret_cast<float*>(row_fm + N);                                            // [WG][warp][2 R]
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = a.q_heads / a.c.heads;
@@ -170,15 +182,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   const int head = blockIdx.y / tiles, tile = blockIdx.y % tiles;
   const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
   if (!sp.ok) {                                   // the sequence's rows see no text token
-    if (part == 0 && tile == 0) {
-      if (threadIdx.x == 0) report(a.status);
-      const int end = __ldg(a.b.row_starts + seq + 1);
-      if (sp.first < 0 || end > a.b.n_rows) return;
-      for (int row = sp.first; row < end; ++row)
-        for (int i = threadIdx.x; i < G * (D / 4); i += Sh::kThreads)
-          finish4<false>(a, (long long)row * a.q_heads + head * G + i / (D / 4), i % (D / 4) * 4,
-                         make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
-    }
+    if (part == 0 && tile == 0) finish_misfit<false, D>(a, sp, seq, head, G);
     return;
   }
   const int M = sp.rows * G, row0 = tile * N, before = sp.len - sp.rows;
@@ -186,64 +190,134 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   if (row0 >= M || t0 >= sp.len) return;
   const int n_tiles = (min(sp.len - t0, parts.tokens) + TT - 1) / TT;
 
-  // ---- set up: barriers, tensor memory, the queries' operand ----
-  if (kCoded && threadIdx.x < 64)
-    reinterpret_cast<uint32_t*>(factors)[threadIdx.x] = half_factor(threadIdx.x == 63 ? 255u : 128u - threadIdx.x, 128u) * 0x10001u;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < Sh::kSlots; ++i) {
-      tc::mbar_init(&bars->slot_full[i], 1);
-      tc::mbar_init(&bars->slot_scaled[i], 1);
-      tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders : 1);
+  // K's tiles come one ahead of V's: K0 K1 V0 K2 V1 .. V(n-1).  Their places in that order:
+  auto place = [&](int i, int kv) { return !kv ? max(2 * i - 1, 0) : (i < n_tiles - 1 ? 2 * i + 2 : 2 * n_tiles - 1); };
+
+  auto tile_at = [&](int pos, int& i, int& kv) {   // and the other way
+    kv = pos == 2 * n_tiles - 1 || (pos && pos % 2 == 0);
+    i = kv ? (pos == 2 * n_tiles - 1 ? n_tiles - 1 : pos / 2 - 1) : (pos + 1) / 2;
+  };
+
+  // ---- the producer's copies ----
+  const int page_tokens = 1 << a.c.page_log2, run = min(page_tokens, Sh::kPart), runs = TT / run, of_part = Sh::kPart / run;
+  bool copies_ok = true;
+  int issued = 0;
+      long long at = 0, at_next = 0;                 // the lane's run of this V's and the next K's tile
+      uint32_t good = 0, good_next = 0;              // the lanes whose runs are there
+      auto find = [&](int i) {                       // a lane copies a run of tokens, which never leaves its page
+        const int t = t0 + i * TT + lane * run;
+        const bool there = lane < runs && t < sp.len;
+        const int page = there ? __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2)) : -1;
+        const bool in = there && page >= 0 && page < a.c.n_pages;
+        if (there && !in) report(a.status);
+        const uint32_t bad = __reduce_or_sync(~0u, there && !in ? ((1u << run / 16) - 1) << (lane * run / 16) : 0u);
+        if (lane == 0) absent_of[i & 15] = bad;
+        good_next = __ballot_sync(~0u, in);
+        at_next = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & (page_tokens - 1));
+      };
+      auto copy = [&](int kv, int pos) {
+        const long long from = kv ? at : at_next;
+        const uint32_t mask = kv ? good : good_next;
+        for (int half = 0; half < Sh::kParts && copies_ok; ++half) {
+          const int s = Sh::kParts * pos + half, slot = s % Sh::kSlots, round = s / Sh::kSlots;
+          if (round) copies_ok = wait(&bars->slot_free[slot], (round - 1) & 1, dead);
+          copies_ok = __all_sync(~0u, copies_ok);
+          if (!copies_ok) break;
+          const int mine = __popc(mask >> (half * of_part) & ((2u << (of_part - 1)) - 1));
+          if (lane == 0) tc::mbar_expect_tx(&bars->slot_full[slot], mine * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
+          issued = s + 1;
+          __syncwarp();
+          if ((mask >> lane & 1) && lane / of_part == half) {
+            unsigned char* to = slots + slot * Sh::kSlot;
+            const int in = lane % of_part * run;      // the run's place in the slot
+            if constexpr (kCoded) {
+              tc::bulk_load(to + in * Sh::kRow, a.c.pages[kv] + from * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
+              tc::bulk_load(to + Sh::kRaw + in * (D / kGroup), a.c.scales[kv] + from * (D / kGroup), run * (D / kGroup),
+                            &bars->slot_full[slot]);
+            } else {
+  #pragma unroll
+              for (int b = 0; b < Sh::kBlocks; ++b)
+                tc::tma_load_2d(to + b * Sh::kBlock + in * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)from);
+            }
+          }
+        }
+      };
+
+  // ---- set up: barriers and the first copy, tensor memory, the queries' operand ----
+  constexpr int kProducer = 4 * Sh::kWGs, kIssuer = kProducer + 1;
+  if (warp == kProducer) {
+    if (lane == 0) {
+      for (int i = 0; i < Sh::kSlots; ++i) {
+        tc::mbar_init(&bars->slot_full[i], 1);
+        tc::mbar_init(&bars->slot_scaled[i], 1);
+        tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders / 2 : 1);
+      }
+      for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->tops_full[i], 1);
+      for (int i = 0; i < 3; ++i) {                // K's operand, V's (one or two)
+        tc::mbar_init(&bars->op_full[i], kCoded ? Sh::kDecoders : 1);
+        tc::mbar_init(&bars->op_free[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) tc::mbar_init(&bars->s_full[i], 1);
+      tc::mbar_init(&bars->p_full, 128 * Sh::kWGs);
+      tc::mbar_init(&bars->pv_done, 1);
+      tc::mbar_init(&bars->drain, 1);
+      tc::fence_mbar_init();
+      *dead = 0;
+      odd_nodes[0] = odd_nodes[1] = 0;
+      *odd_tile = 0;
     }
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->tops_full[i], 1);
-    for (int i = 0; i < 3; ++i) {                  // K's operand, V's (one or two)
-      tc::mbar_init(&bars->op_full[i], kCoded ? Sh::kDecoders : 1);
-      tc::mbar_init(&bars->op_free[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&bars->s_full[i], 1);
-    tc::mbar_init(&bars->p_full, 128 * Sh::kWGs);
-    tc::mbar_init(&bars->pv_done, 1);
-    tc::mbar_init(&bars->drain, 1);
-    tc::fence_mbar_init();
-    *dead = 0;
-    odd_nodes[0] = odd_nodes[1] = 0;
-  }
-  if (warp == 4 * Sh::kWGs + 1) tc::tmem_alloc(tmem_slot, Sh::kTmem);
-  for (int n = warp; n < N; n += Sh::kThreads / 32) {   // a warp per row: lane i has elements i * D/32 ..
-    constexpr int E = D / 32;
-    const int row = row0 + n;
-    const bool in = row < M;
-    const int node = in ? row / G : 0;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (long long)(sp.first + node) * a.q_token +
-                             (long long)(head * G + (in ? row % G : 0)) * a.q_head + lane * E;
-    uint32_t w[E / 2], top = 0;
+    __syncwarp();
+    find(0);
+    copy(0, 0);
+  } else if (warp == kIssuer) {
+    tc::tmem_alloc(tmem_slot, Sh::kTmem);
+  } else {
+    constexpr int E = D / 32, kStagers = Sh::kThreads / 32 - 2, kMine = (N + kStagers - 1) / kStagers;
+    const int stager = warp < kProducer ? warp : warp - 2;
+    uint32_t w[kMine][E / 2];                      // a warp per row, lane i with its elements i * E ..; all rows' loads first
+    unsigned long long word[kMine];
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      w[i] = in ? reinterpret_cast<const uint32_t*>(q)[i] : 0u;
-      top = max(top, max(w[i] << 16 & 0x7FFF0000u, w[i] & 0x7FFF0000u));
+    for (int x = 0; x < kMine; ++x) {
+      const int n = stager + x * kStagers, row = row0 + n;
+      const bool in = n < N && row < M;
+      const int node = in ? row / G : 0;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (long long)(sp.first + node) * a.q_token +
+                               (long long)(head * G + (in ? row - node * G : 0)) * a.q_head + lane * E;
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) w[x][i] = in ? reinterpret_cast<const uint32_t*>(q)[i] : 0u;
+      word[x] = a.tree ? a.tree[sp.first + node] : (node >= 63 ? ~0ull : (2ull << node) - 1);
     }
-    float back = kToLog2;
-    if constexpr (kCoded) {                        // largest element into [2^14, 2^15)
-      const int E8 = (int)(__reduce_max_sync(~0u, top) >> 23);
-      const int e = E8 == 255 || __reduce_max_sync(~0u, top) == 0 ? 0 : max(-126, min(126, 141 - E8));
-      const float f = __uint_as_float((uint32_t)(127 + e) << 23);
-      back *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      const int n = stager + x * kStagers;
+      if (n >= N) break;
+      float back = kToLog2;
+      if constexpr (kCoded) {                      // largest element into [2^14, 2^15)
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) top = max(top, max(w[x][i] << 16 & 0x7FFF0000u, w[x][i] & 0x7FFF0000u));
+        top = __reduce_max_sync(~0u, top);
+        const int E8 = (int)(top >> 23), e = E8 == 255 || top == 0 ? 0 : max(-126, min(126, 141 - E8));
+        const float f = __uint_as_float((uint32_t)(127 + e) << 23);
+        back *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          const float2 v = unpack_bf16x2(w[x][i]);
+          w[x][i] = pack2<true>(v.x * f, v.y * f);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        const float2 v = unpack_bf16x2(w[i]);
-        w[i] = pack2<true>(v.x * f, v.y * f);
+        const int d = lane * E + 2 * i;
+        *reinterpret_cast<uint32_t*>(q_op + d / 64 * (N * 128) + n * 128 + ((d % 64 / 8) ^ (n & 7)) * 16 + d % 8 * 2) = w[x][i];
+      }
+      if (lane == 0) {
+        row_fm[n] = make_float2(back, 0.f);
+        words[n] = word[x];
       }
     }
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const int d = lane * E + 2 * i;
-      *reinterpret_cast<uint32_t*>(q_op + d / 64 * (N * 128) + n * 128 + ((d % 64 / 8) ^ (n & 7)) * 16 + d % 8 * 2) = w[i];
-    }
-    if (lane == 0) {
-      row_factor[n] = back;
-      m_ref[n] = -FLT_MAX;                         // every score is far above it
-      words[n] = a.tree ? a.tree[sp.first + node] : (node >= 63 ? ~0ull : (2ull << node) - 1);
-    }
+    if (kCoded && threadIdx.x < 64)
+      reinterpret_cast<uint32_t*>(factors)[threadIdx.x] = half_factor(threadIdx.x == 63 ? 255u : 128u - threadIdx.x, 128u) * 0x10001u;
   }
   tc::fence_proxy_async();
   tc::fence_before_sync();
@@ -251,50 +325,20 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 4 * Sh::kWGs) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------------------------ producer ---
-    const int page_tokens = 1 << a.c.page_log2, run = min(page_tokens, Sh::kPart), runs = TT / run, of_part = Sh::kPart / run;
-    bool ok = true;
-    int issued = 0;
-    for (int i = 0; i < n_tiles && ok; ++i) {
-      const int t = t0 + i * TT + lane * run;      // a lane copies a run of tokens, which never leaves its page
-      const bool there = lane < runs && t < sp.len;
-      const int page = there ? __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2)) : -1;
-      const bool good = there && page >= 0 && page < a.c.n_pages;
-      if (there && !good) report(a.status);
-      const uint32_t bad = __reduce_or_sync(~0u, there && !good ? ((1u << run / 16) - 1) << (lane * run / 16) : 0u);
-      const uint32_t copies = __ballot_sync(~0u, good);
-      const long long at = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & (page_tokens - 1));
-      if (lane == 0) absent_of[i & 15] = bad;
-      for (int x = 0; x < 2 * Sh::kParts && ok; ++x) {
-        const int s = 2 * Sh::kParts * i + x, kv = x / Sh::kParts, half = x % Sh::kParts;
-        const int slot = s % Sh::kSlots, round = s / Sh::kSlots;
-        if (round) ok = wait(&bars->slot_free[slot], (round - 1) & 1, dead);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        const int mine = __popc(copies >> (half * of_part) & ((2u << (of_part - 1)) - 1));
-        if (lane == 0) tc::mbar_expect_tx(&bars->slot_full[slot], mine * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
-        issued = s + 1;
-        __syncwarp();
-        if (good && lane / of_part == half) {
-          unsigned char* to = slots + slot * Sh::kSlot;
-          const int in = lane % of_part * run;      // the run's place in the slot
-          if constexpr (kCoded) {
-            tc::bulk_load(to + in * Sh::kRow, a.c.pages[kv] + at * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
-            tc::bulk_load(to + Sh::kRaw + in * (D / kGroup), a.c.scales[kv] + at * (D / kGroup), run * (D / kGroup),
-                          &bars->slot_full[slot]);
-          } else {
-#pragma unroll
-            for (int b = 0; b < Sh::kBlocks; ++b)
-              tc::tma_load_2d(to + b * Sh::kBlock + in * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)at);
-          }
-        }
+    for (int i = 0; i < n_tiles && copies_ok; ++i) {
+      at = at_next, good = good_next;
+      if (i + 1 < n_tiles) {
+        find(i + 1);
+        copy(0, place(i + 1, 0));
       }
+      if (copies_ok) copy(1, place(i, 1));
     }
     // Copies in flight when a wait expired land before the block ends.
-    if (!ok)
+    if (!copies_ok)
       for (int s = max(0, issued - Sh::kSlots); s < issued; ++s) wait(&bars->slot_full[s % Sh::kSlots], s / Sh::kSlots & 1, nullptr);
-  } else if (warp == 4 * Sh::kWGs + 1) {
+  } else if (warp == kIssuer) {
     // -------------------------------------------------------------------------------- issuer ---
     if (lane == 0) {
       constexpr uint32_t kIdS = kCoded ? tc::idesc_f16(128, N, false) : tc::idesc_bf16(128, N, false);
@@ -304,14 +348,14 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       const uint32_t q_addr = tc::smem_u32(q_op), p_addr = tc::smem_u32(p_op);
       auto op = [&](int i, int kv) { return kv ? 1 + i % Sh::kVOps : 0; };
       auto operand = [&](int i, int kv) {
-        return tc::smem_u32(kCoded ? k_op + op(i, kv) * Sh::kOp : slots + (2 * i + kv) % Sh::kSlots * Sh::kSlot);
+        return tc::smem_u32(kCoded ? k_op + op(i, kv) * Sh::kOp : slots + place(i, kv) % Sh::kSlots * Sh::kSlot);
       };
       auto full = [&](int i, int kv) {
         return kCoded ? wait(&bars->op_full[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, dead)
-                      : wait(&bars->slot_full[(2 * i + kv) % Sh::kSlots], (2 * i + kv) / Sh::kSlots & 1, dead);
+                      : wait(&bars->slot_full[place(i, kv) % Sh::kSlots], place(i, kv) / Sh::kSlots & 1, dead);
       };
       auto release = [&](int i, int kv) {
-        tc::mma_commit(kCoded ? &bars->op_free[op(i, kv)] : &bars->slot_free[(2 * i + kv) % Sh::kSlots]);
+        tc::mma_commit(kCoded ? &bars->op_free[op(i, kv)] : &bars->slot_free[place(i, kv) % Sh::kSlots]);
       };
       const uint64_t q_desc = tc::smem_desc(q_addr, 16, 1024, 2), p_desc = tc::smem_desc(p_addr, 16, 8 * N * 2, kSwizzle);
       auto scores = [&](int i) {
@@ -326,12 +370,9 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         release(i, 0);
         return true;
       };
-      // With V's operand in place early the next scores go first and are ready when this softmax is; with one
-      // operand that the decoders fill in turn, this tile's sums do, and the decoders go on with V's next.
-      constexpr bool kAhead = !kCoded || Sh::kVOps == 2;
       bool ok = scores(0);
       for (int i = 0; i < n_tiles && ok; ++i) {
-        if (kAhead && i + 1 < n_tiles) ok = scores(i + 1);
+        if (i + 1 < n_tiles) ok = scores(i + 1);
         if (ok) ok = full(i, 1);
         if (ok) ok = wait(&bars->p_full, i & 1, dead);
         if (!ok) break;
@@ -345,7 +386,6 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
                          kIdO, i > 0 || k > 0);
         tc::mma_commit(&bars->pv_done);
         release(i, 1);
-        if (!kAhead && i + 1 < n_tiles) ok = scores(i + 1);
       }
       if (!ok) {                                   // products in flight end before tensor memory is released
         tc::mma_commit(&bars->drain);
@@ -360,7 +400,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     float l[R] = {}, high[R];                      // the thread's tokens' sum, and maximum less the reference
 #pragma unroll
     for (int n = 0; n < R; ++n) high[n] = -INFINITY;
-    uint32_t ref = 0;
+    uint32_t ref = 0, unset = (1u << R) - 1;       // rows that have seen no score yet (their reference is 0)
     bool ok = true;
     for (int i = 0; i < n_tiles; ++i) {
       ok = wait(&bars->s_full[i & 1], i / 2 & 1, dead);
@@ -378,18 +418,18 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         v_top = tops[((i & 3) * 2 + 1) * TT + tid];
       }
       float x[R];
-      auto scores = [&]() {                        // x: the scores less the reference
-        tc::tmem_ld<R>(lanes + (i & 1) * N + rows0, x);
-        tc::tmem_ld_wait();
+      tc::tmem_ld<R>(lanes + (i & 1) * N + rows0, x);
+      tc::tmem_ld_wait();
 #pragma unroll
-        for (int n = 0; n < R; ++n) x[n] = fmaf(x[n], k_scale * row_factor[rows0 + n], -m_ref[rows0 + n]);
-        if (tail || bad) {
+      for (int n = 0; n < R; n += 2) {             // the scores less the references
+        const float4 f = *reinterpret_cast<const float4*>(row_fm + rows0 + n);
+        x[n] = fmaf(x[n], k_scale * f.x, f.y), x[n + 1] = fmaf(x[n + 1], k_scale * f.z, f.w);
+      }
+      if (tail || bad) {
 #pragma unroll
-          for (int n = 0; n < R; ++n)
-            if (absent || (node >= 0 && !(words[rows0 + n] >> node & 1))) x[n] = -INFINITY;
-        }
-      };
-      scores();
+        for (int n = 0; n < R; ++n)
+          if (absent || (node >= 0 && !(words[rows0 + n] >> node & 1))) x[n] = -INFINITY;
+      }
       if (i) {                                     // O is whole, and P's place free
         ok &= wait(&bars->pv_done, (i - 1) & 1, dead);
         ok = __all_sync(~0u, ok);
@@ -398,80 +438,59 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       float most = -INFINITY;
 #pragma unroll
       for (int n = 0; n < R; ++n) most = fmaxf(most, x[n]);
-      if (bar_or(bar, 128, most > kSlack || v_top > ref || !ok)) {
-        if (bar_or(bar, 128, !ok)) break;
-        // move the references: of the rows with such a score, to the largest of this tile; of V's scales, to the largest
-        float v[R];
+      bool move = most > kSlack || v_top > ref || !ok;
+      if (unset) {
 #pragma unroll
-        for (int n = 0; n < R; ++n) v[n] = x[n];
-        const float up = reduce_rows<true>(v);
+        for (int n = 0; n < R; ++n) move |= (unset >> n & 1) && x[n] > -INFINITY;
+      }
+      if (bar_or(bar, 128, move)) {
+        if (bar_or(bar, 128, !ok)) break;
+        // move the references: of the rows with such a score, to this tile's largest; of V's scales, to the largest
         float* mine = exchange + (wg * 4 + (warp & 3)) * 2 * R;
-        if (lane < R) mine[lane] = up;
+#pragma unroll
+        for (int n = 0; n < R; n += 4) {
+          const float4 v = make_float4(warp_max(x[n]), warp_max(x[n + 1]), warp_max(x[n + 2]), warp_max(x[n + 3]));
+          if (lane == 0) *reinterpret_cast<float4*>(mine + n) = v;
+        }
         const uint32_t top = __reduce_max_sync(~0u, v_top);
         if (lane == 0) mine[R] = __uint_as_float(top);
         bar_sync(bar);
+        const float* all = exchange + wg * 4 * 2 * R;
         uint32_t new_ref = ref;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) new_ref = max(new_ref, __float_as_uint(exchange[(wg * 4 + w) * 2 * R + R]));
-        float keep = 1.f;                          // of row rows0 + tid
-        if (tid < R) {
-          float by = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) by = fmaxf(by, exchange[(wg * 4 + w) * 2 * R + tid]);
-          if (by > kSlack) {
-            const float old = m_ref[rows0 + tid], next = old == -FLT_MAX ? -INFINITY : old + by;
-            m_ref[rows0 + tid] = next;
-            keep = old == -FLT_MAX ? 0.f : exp2_fast(old - next);
-          }
-        }
-        bar_sync(bar);                             // the exchanged maxima are read
-        if (tid < R) exchange[wg * 4 * 2 * R + tid] = keep;
-        bar_sync(bar);
-        const float* keeps = exchange + wg * 4 * 2 * R;
-        // A row's first reference: the scores less -FLT_MAX have lost their digits, so the maximum is taken again.
-        bool first = false;
-#pragma unroll
-        for (int n = 0; n < R; ++n) first |= m_ref[rows0 + n] == -INFINITY;
-        if (first) {
-          tc::tmem_ld<R>(lanes + (i & 1) * N + rows0, v);
-          tc::tmem_ld_wait();
-#pragma unroll
-          for (int n = 0; n < R; ++n) {
-            v[n] *= k_scale * row_factor[rows0 + n];
-            if (absent || (node >= 0 && !(words[rows0 + n] >> node & 1))) v[n] = -INFINITY;
-          }
-          const float z = reduce_rows<true>(v);
-          if (lane < R) exchange[(wg * 4 + (warp & 3)) * 2 * R + R + lane] = z;
-          bar_sync(bar);
-          if (tid < R && m_ref[rows0 + tid] == -INFINITY) {
-            float by = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) by = fmaxf(by, exchange[(wg * 4 + w) * 2 * R + R + tid]);
-            m_ref[rows0 + tid] = by;
-          }
-          bar_sync(bar);
-        }
+        for (int w = 0; w < 4; ++w) new_ref = max(new_ref, __float_as_uint(all[w * 2 * R + R]));
         const float down = kCoded ? __uint_as_float((uint32_t)max(127 + (int)ref - (int)new_ref, 0) << 23) : 1.f;
         ref = new_ref;
+        float keep[R];
 #pragma unroll
         for (int n = 0; n < R; ++n) {
-          if (keeps[n] != 1.f) high[n] = -INFINITY;   // all before is below this tile's largest
-          l[n] *= keeps[n];
+          const float by = fmaxf(fmaxf(all[n], all[2 * R + n]), fmaxf(all[4 * R + n], all[6 * R + n]));
+          const bool first = unset >> n & 1;
+          keep[n] = 1.f;
+          if (by > (first ? -INFINITY : kSlack)) {
+            x[n] -= by;
+            keep[n] = first ? 0.f : exp2_fast(-by);
+            l[n] *= keep[n];
+            high[n] = -INFINITY;                   // all before is below this tile's largest
+            unset &= ~(1u << n);
+            if (tid == n) row_fm[rows0 + n].y -= by;
+          }
+          keep[n] *= down;
         }
         if (i) {
 #pragma unroll
           for (int g = 0; g < Sh::kGroups; ++g) {
             const uint32_t at = lanes + (2 + g) * N + rows0;
+            float v[R];
             tc::tmem_ld<R>(at, v);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int n = 0; n < R; ++n) v[n] *= keeps[n] * down;
+            for (int n = 0; n < R; ++n) v[n] *= keep[n];
             tc::tmem_st16(at, v);
           }
           tc::tmem_st_wait();
         }
-        scores();
-        bar_sync(bar);                             // before the factors' place is written again
+        bar_sync(bar);                             // before the exchange's place is written again
       }
       const float fold = kCoded ? __uint_as_float((uint32_t)max(127 + (int)kBase + (int)v_top - (int)ref, 0) << 23) : 1.f;
       uint32_t w[R / 2];
@@ -488,36 +507,38 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
 #pragma unroll
       for (int y = 0; y < 2; ++y)
         *reinterpret_cast<uint4*>(p_at + (((rows0 / 8 + y) ^ turn) << 4)) = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
-      if (!kCoded && tail && wg == 0) {
-        // Behind the last token V's operand holds whatever the page holds (decoders write zeros there), and
-        // a drafted token's infinities and NaN are for some rows only: zeros take their place.
-        ok = __all_sync(~0u, wait(&bars->slot_full[(2 * i + 1) % Sh::kSlots], (2 * i + 1) / Sh::kSlots & 1, dead));
-      }
-      if (wg == 0 && ok && (absent ? !kCoded : tail && node >= 0)) {
-        if (!tail && !kCoded) ok = wait(&bars->slot_full[(2 * i + 1) % Sh::kSlots], (2 * i + 1) / Sh::kSlots & 1, dead);
-        unsigned char* v = kCoded ? v_op + i % Sh::kVOps * Sh::kOp : slots + (2 * i + 1) % Sh::kSlots * Sh::kSlot;
-        if constexpr (kCoded) ok = wait(&bars->op_full[1 + i % Sh::kVOps], i / Sh::kVOps & 1, dead);
-        bool odd = false;
-        for (int b = 0; b < Sh::kBlocks; ++b)
-          for (int x = 0; x < 8; ++x) {
-            uint4* w = reinterpret_cast<uint4*>(v + b * Sh::kBlock + tid * 128 + x * 16);
-            if (absent) {
-              *w = make_uint4(0, 0, 0, 0);
-            } else {
-              uint32_t y[4] = {w->x, w->y, w->z, w->w};
-              bool here = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (odd2<kCoded>(y[e])) {
-                  here = true;
-                  if (odd2<kCoded>(y[e] & 0xFFFFu)) y[e] &= 0xFFFF0000u;
-                  if (odd2<kCoded>(y[e] & 0xFFFF0000u)) y[e] &= 0xFFFFu;
-                }
-              if (here) *w = make_uint4(y[0], y[1], y[2], y[3]);
-              odd |= here;
-            }
+      // Behind the last token V's operand holds whatever the page holds (decoders write zeros there), and a
+      // drafted token's infinities and NaN are for some rows only: zeros take their place.
+      if (wg == 0 && (tail || (bad && !kCoded))) {
+        ok = wait(kCoded ? &bars->op_full[1 + i % Sh::kVOps] : &bars->slot_full[place(i, 1) % Sh::kSlots],
+                  (kCoded ? i / Sh::kVOps : place(i, 1) / Sh::kSlots) & 1, dead);
+        ok = __all_sync(~0u, ok);
+        unsigned char* v = kCoded ? v_op + i % Sh::kVOps * Sh::kOp : slots + place(i, 1) % Sh::kSlots * Sh::kSlot;
+        const int base = t0 + i * TT, held = min(sp.len - base, TT);
+        if (!kCoded) {
+          const int from = bad ? 0 : held;
+          for (int y = tid; y < (TT - from) * (D / 8); y += 128) {
+            const int tok = from + y / (D / 8), c = y % (D / 8);
+            if (tok >= held || (bad >> (tok / 16) & 1))
+              *reinterpret_cast<uint4*>(v + c / 8 * Sh::kBlock + tok * 128 + c % 8 * 16) = make_uint4(0, 0, 0, 0);
           }
-        if (odd) atomicOr(odd_nodes + (node >> 5), 1u << (node & 31));
+        }
+        const int from = max(before - base, 0);
+        for (int y = tid; (!kCoded || *odd_tile) && y < (held - from) * (D / 8); y += 128) {
+          const int tok = from + y / (D / 8), c = y % (D / 8);
+          uint4* at = reinterpret_cast<uint4*>(v + c / 8 * Sh::kBlock + tok * 128 + c % 8 * 16);
+          uint32_t u[4] = {at->x, at->y, at->z, at->w};
+          if ((bad >> (tok / 16) & 1) || !(odd2<kCoded>(u[0]) || odd2<kCoded>(u[1]) || odd2<kCoded>(u[2]) || odd2<kCoded>(u[3])))
+            continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (odd2<kCoded>(u[e] & 0xFFFFu)) u[e] &= 0xFFFF0000u;
+            if (odd2<kCoded>(u[e] & 0xFFFF0000u)) u[e] &= 0xFFFFu;
+          }
+          *at = make_uint4(u[0], u[1], u[2], u[3]);
+          const int j = base + tok - before;
+          atomicOr(odd_nodes + (j >> 5), 1u << (j & 31));
+        }
       }
       tc::fence_proxy_async();
       tc::fence_before_sync();
@@ -544,8 +565,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
           sum += exchange[(wg * 4 + w) * 2 * R + R + tid];
         }
         const float to = m == -INFINITY ? 0.f : exp2f(-m);
-        row_ml[rows0 + tid] = make_float2(m == -INFINITY ? m : m_ref[rows0 + tid] + m, sum * to);
-        row_factor[rows0 + tid] = to * (kCoded ? scale_value(ref) * 0.015625f : 1.f);   // of the row's sums
+        row_ml[rows0 + tid] = make_float2(m == -INFINITY ? m : m - row_fm[rows0 + tid].y, sum * to);
+        row_fm[rows0 + tid].x = to * (kCoded ? scale_value(ref) * 0.015625f : 1.f);   // of the row's sums
       }
       bar_sync(bar);
       float* sums = reinterpret_cast<float*>(kCoded ? smem : slots);
@@ -556,11 +577,11 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         tc::tmem_ld_wait();
         if (g * 128 + tid < D) {
 #pragma unroll
-          for (int n = 0; n < R; ++n) sums[(rows0 + n) * (D + 4) + g * 128 + tid] = o[n] * row_factor[rows0 + n];
+          for (int n = 0; n < R; ++n) sums[(rows0 + n) * (D + 4) + g * 128 + tid] = o[n] * row_fm[rows0 + n].x;
         }
       }
       // Infinities and NaN of drafted tokens, for the rows that see them (rare): p by one thread a row.
-      for (int j = 0; j < sp.rows; ++j) {
+      for (int j = 0; (odd_nodes[0] | odd_nodes[1]) && j < sp.rows; ++j) {
         if (!(odd_nodes[j >> 5] >> (j & 31) & 1)) continue;
         const int t = before + j;
         if (t < t0 || t >= t0 + n_tiles * TT) continue;
@@ -589,22 +610,28 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         }
       }
       bar_sync(bar);
-      for (int i = tid; i < R * (D / 4); i += 128) {
-        const int n = rows0 + i / (D / 4), d = i % (D / 4) * 4, row = row0 + n;
-        if (row >= M) break;
-        const float4 v = *reinterpret_cast<const float4*>(sums + n * (D + 4) + d);
+      // eight threads to a row
+      const int n = rows0 + tid / 8, row = row0 + n;
+      if (row < M) {
         const float2 ml = row_ml[n];
+        const float* from = sums + n * (D + 4) + tid % 8 * 4;
         if (parts.count == 1) {
-          finish4<false>(a, (long long)(sp.first + row / G) * a.q_heads + head * G + row % G, d, v, ml.x, ml.y);
+          const long long at = (long long)(sp.first + row / G) * a.q_heads + head * G + row % G;
+          const RowEnd e = end_row(a, at, ml.x, ml.y, tid % 8 == 0);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            finish4<false>(a, at, tid % 8 * 4 + 32 * k, *reinterpret_cast<const float4*>(from + 32 * k), e);
         } else {
           const long long to = ((long long)part * gridDim.z * gridDim.y + seq * gridDim.y + blockIdx.y) * N + n;
-          *reinterpret_cast<float4*>(parts.o + to * D + d) = v;
-          if (d == 0) parts.ml[to] = ml;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            *reinterpret_cast<float4*>(parts.o + to * D + tid % 8 * 4 + 32 * k) = *reinterpret_cast<const float4*>(from + 32 * k);
+          if (tid % 8 == 0) parts.ml[to] = ml;
         }
       }
     }
     tc::fence_before_sync();
-  } else if (kCoded && warp == 4 * Sh::kWGs + 2) {
+  } else if (kCoded && warp == kIssuer + 1) {
     // -------------------------------------------------------------------------------- scaler ---
     // A lane takes a token: the largest of its scales (the NaN scale aside), and in the scales' place every
     // group's distance to it (31: 2^-25 and less are 0 in half precision; 63: NaN).
@@ -612,7 +639,9 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       constexpr int kGroupsRow = D / kGroup;
       bool ok = true;
       for (int s = 0; s < 4 * n_tiles && ok; ++s) {
-        const int i = s / 4, kv = s / 2 & 1, half = s & 1, slot = s % Sh::kSlots;
+        int i, kv;
+        tile_at(s / 2, i, kv);
+        const int half = s & 1, slot = s % Sh::kSlots;
         ok = __all_sync(~0u, wait(&bars->slot_full[slot], s / Sh::kSlots & 1, dead));
         if (!ok) break;
         const int held = sp.len - (t0 + i * TT);
@@ -660,19 +689,22 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     // ------------------------------------------------------------------------------ decoders ---
     // A lane takes a group of 32 values at a time.  Eight lanes take four tokens' two groups of a 64-column block, and
     // odd tokens their halves in the other order, so that stores of 16 bytes never meet in a bank.
-    constexpr int kAll = 32 * Sh::kDecoders, kGroupsRow = D / kGroup;
+    // Half of the decoders take a tile's first 64 tokens, the others the rest.
+    constexpr int kAll = 16 * Sh::kDecoders, kGroupsRow = D / kGroup;
     constexpr int kItems = Sh::kPart / 4 * Sh::kBlocks;                    // of eight lanes, in a slot
     constexpr int kPasses = (kItems + kAll / 8 - 1) / (kAll / 8);
-    const int me = threadIdx.x - 32 * (4 * Sh::kWGs + 3);
+    const int of = threadIdx.x - 32 * (4 * Sh::kWGs + 3), half = of / kAll, me = of % kAll;
     bool ok = true;
-    for (int s = 0; s < 4 * n_tiles && ok; ++s) {
-      const int i = s / 4, kv = s / 2 & 1, half = s & 1, slot = s % Sh::kSlots;
+    for (int pos = 0; pos < 2 * n_tiles && ok; ++pos) {
+      int i, kv;
+      tile_at(pos, i, kv);
+      const int s = 2 * pos + half, slot = s % Sh::kSlots;
       const int op = kv ? 1 + i % Sh::kVOps : 0, turn = kv ? i / Sh::kVOps : i;
       ok = wait(&bars->slot_scaled[slot], s / Sh::kSlots & 1, dead);
-      if (!half && turn) ok &= wait(&bars->op_free[op], (turn - 1) & 1, dead);
+      if (turn) ok &= wait(&bars->op_free[op], (turn - 1) & 1, dead);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
-      const int held = sp.len - (t0 + i * TT + half * Sh::kPart);
+      const int t_half = t0 + i * TT + half * Sh::kPart, held = sp.len - t_half;
       const uint32_t bad = absent_of[i & 15] >> (half * (Sh::kPart / 16));
       const bool whole = held >= Sh::kPart && !(bad & ((1u << Sh::kPart / 16) - 1));
       const unsigned char* raw = slots + slot * Sh::kSlot;
@@ -684,6 +716,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         const int block = item % Sh::kBlocks, tok = item / Sh::kBlocks * 4 + me % 8 / 2, g = block * 2 + me % 2;
         const uint32_t f = reinterpret_cast<const uint32_t*>(factors)[raw[Sh::kRaw + tok * kGroupsRow + g]];
         const bool absent = !whole && (tok >= held || (bad >> (tok / 16) & 1));
+        const bool drafted = kv && t_half + tok >= before;
+        uint32_t odd = 0;
         unsigned char* to = out + block * Sh::kBlock + tok * 128;
         const int chunk = me % 2 * 4;
         if constexpr (FMT == kFp8) {
@@ -698,9 +732,11 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
             unpack_e4m3x4(w.z, h[4], h[5]);
             unpack_e4m3x4(w.w, h[6], h[7]);
 #pragma unroll
+            for (int z = 0; z < 8; ++z) h[z] = mul_half2(h[z], f);
+#pragma unroll
             for (int z = 0; z < 2; ++z)
-              *reinterpret_cast<uint4*>(to + ((chunk + part * 2 + z) ^ (tok & 7)) * 16) =
-                  make_uint4(mul_half2(h[4 * z], f), mul_half2(h[4 * z + 1], f), mul_half2(h[4 * z + 2], f), mul_half2(h[4 * z + 3], f));
+              *reinterpret_cast<uint4*>(to + ((chunk + part * 2 + z) ^ (tok & 7)) * 16) = make_uint4(h[4 * z], h[4 * z + 1], h[4 * z + 2], h[4 * z + 3]);
+            if (drafted) odd |= odd8(h);
           }
         } else {
           uint4 w = *reinterpret_cast<const uint4*>(raw + tok * Sh::kRow + g * 16);
@@ -710,21 +746,24 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
           for (int z = 0; z < 4; ++z) {
             uint32_t h[4];
             unpack_e2m1x8(in[z], h);
-            *reinterpret_cast<uint4*>(to + ((chunk + z) ^ (tok & 7)) * 16) =
-                make_uint4(mul_half2(h[0], f), mul_half2(h[1], f), mul_half2(h[2], f), mul_half2(h[3], f));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = mul_half2(h[e], f);
+            *reinterpret_cast<uint4*>(to + ((chunk + z) ^ (tok & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
           }
+          odd = drafted && (f & 0x7C00u) == 0x7C00u;   // E2M1 itself has no infinity or NaN
         }
+        if (odd) *odd_tile = 1;
       }
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
-        if (half) tc::mbar_arrive(&bars->op_full[op]);
+        tc::mbar_arrive(&bars->op_full[op]);
         tc::mbar_arrive(&bars->slot_free[slot]);
       }
     }
   }
   __syncthreads();
-  if (warp == 4 * Sh::kWGs + 1) {
+  if (warp == kIssuer) {
     tc::fence_after_sync();
     tc::tmem_free(tmem, Sh::kTmem);
   }
