@@ -9,7 +9,7 @@
 //   softmax (4 or 8)  S^T from tensor memory -> P in shared memory; running maximum and sum in registers
 //   producer (1)      copies pages: TMA tiles into operand slots (bfloat16), bulk copies into raw slots (coded)
 //   issuer (1)        all products; the next tile's S^T is issued before this tile's O^T waits for its softmax
-//   scaler (1)        coded caches: each token's largest scale, and its groups' distances to it
+//   scalers (2)       coded caches: each token's largest scale, and its groups' distances to it
 //   decoders (8, 16)  coded caches: raw slots -> half-precision operands, once for all rows of the unit
 // Every wait is bounded; one that expires records TACTKV_TIMEOUT and ends the block's work.
 //
@@ -35,6 +35,7 @@ namespace {
 constexpr int D = TACTKV_TEXT_D;
 constexpr int TT = 128;                           // tokens of a tile
 constexpr int kMaxSlots = 12;
+constexpr int kScalers = 2;                       // one for each half of a tile
 constexpr int R = 16;                             // rows of a softmax warpgroup
 constexpr float kToLog2 = to_log2(D);
 constexpr uint32_t kPolls = 1u << 16;             // of a wait; each suspends the thread for up to kPause ns
@@ -64,7 +65,7 @@ struct Shape {
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;        // V operands in turn
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
   static constexpr int kDecoders = !kCoded ? 0 : (N <= 32 && kCtas == 1 ? 16 : 8);
-  static constexpr int kThreads = 32 * (4 * kWGs + 2 + (kCoded ? 1 + kDecoders : 0));
+  static constexpr int kThreads = 32 * (4 * kWGs + 2 + (kCoded ? kScalers + kDecoders : 0));
   static constexpr int kFit = ((kCtas == 2 ? 113 : 227) * 1024 - kRest - kOps) / kSlot;
   static constexpr int kSlots = kFit > kMaxSlots ? kMaxSlots : kFit;
   static constexpr int kSmem = kRest + kOps + kSlots * kSlot;
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         tc::mbar_init(&bars->slot_scaled[i], 1);
         tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders / 2 : 1);
       }
-      for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->tops_full[i], 1);
+      for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->tops_full[i], kScalers);
       for (int i = 0; i < 3; ++i) {                // K's operand, V's (one or two)
         tc::mbar_init(&bars->op_full[i], kCoded ? Sh::kDecoders : 1);
         tc::mbar_init(&bars->op_free[i], 1);
@@ -631,17 +632,18 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       }
     }
     tc::fence_before_sync();
-  } else if (kCoded && warp == kIssuer + 1) {
+  } else if (kCoded && warp <= kIssuer + kScalers) {
     // -------------------------------------------------------------------------------- scaler ---
     // A lane takes a token: the largest of its scales (the NaN scale aside), and in the scales' place every
     // group's distance to it (31: 2^-25 and less are 0 in half precision; 63: NaN).
     if constexpr (kCoded) {
       constexpr int kGroupsRow = D / kGroup;
       bool ok = true;
-      for (int s = 0; s < 4 * n_tiles && ok; ++s) {
+      const int half = warp - kIssuer - 1;
+      for (int pos = 0; pos < 2 * n_tiles && ok; ++pos) {
         int i, kv;
-        tile_at(s / 2, i, kv);
-        const int half = s & 1, slot = s % Sh::kSlots;
+        tile_at(pos, i, kv);
+        const int s = 2 * pos + half, slot = s % Sh::kSlots;
         ok = __all_sync(~0u, wait(&bars->slot_full[slot], s / Sh::kSlots & 1, dead));
         if (!ok) break;
         const int held = sp.len - (t0 + i * TT);
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         __syncwarp();
         if (lane == 0) {
           tc::mbar_arrive(&bars->slot_scaled[slot]);
-          if (kv && half) tc::mbar_arrive(&bars->tops_full[i & 3]);
+          if (kv) tc::mbar_arrive(&bars->tops_full[i & 3]);
         }
       }
     }
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     constexpr int kAll = 16 * Sh::kDecoders, kGroupsRow = D / kGroup;
     constexpr int kItems = Sh::kPart / 4 * Sh::kBlocks;                    // of eight lanes, in a slot
     constexpr int kPasses = (kItems + kAll / 8 - 1) / (kAll / 8);
-    const int of = threadIdx.x - 32 * (4 * Sh::kWGs + 3), half = of / kAll, me = of % kAll;
+    const int of = threadIdx.x - 32 * (kIssuer + 1 + kScalers), half = of / kAll, me = of % kAll;
     bool ok = true;
     for (int pos = 0; pos < 2 * n_tiles && ok; ++pos) {
       int i, kv;
