@@ -54,12 +54,13 @@ struct Shape {
   static constexpr int kRaw = kPart * kRow, kRawScales = kPart * (D / kGroup);
   static constexpr int kSlot = kCoded ? kRaw + kRawScales : kOp;
   static constexpr int kQ = kBlocks * N * 128, kP = TT * N * 2;
+  static constexpr int kPs = kCoded && D == 256 && N == 32 ? 1 : 2;             // P's places, in turn (as many as fit)
   static constexpr int kFactors = kCoded ? 256 : 0;                            // 2^-i, twice in half precision
   static constexpr int kTops = kCoded ? 8 * TT : 0;                            // [tile % 4][K, V][token]
   static constexpr int kMisc = 1024 + 24 * N + kWGs * 4 * 8 * R;
   // With an odd number of blocks the last product reads a block past V's operand: something must be there.
   static constexpr int kPad = kBlocks % 2 ? kBlock : 0;
-  static constexpr int kRest = 1024 + kQ + kP + kFactors + kTops + kMisc + kPad;
+  static constexpr int kRest = 1024 + kQ + kPs * kP + kFactors + kTops + kMisc + kPad;
   // Two blocks on an SM where two slots fit each: one's start, end and waits are the other's time.
   static constexpr int kCtas = N <= (kCoded ? 16 : 32) && kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot <= 113 * 1024 ? 2 : 1;
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;        // V operands in turn
@@ -77,7 +78,7 @@ struct Shape {
 
 struct Bars {
   uint64_t slot_full[kMaxSlots], slot_scaled[kMaxSlots], slot_free[kMaxSlots], op_full[3], op_free[3], tops_full[4],
-      s_full[2], p_full, pv_done, drain;
+      s_full[2], p_full[2], pv_done[2], drain;
 };
 static_assert(sizeof(Bars) <= 512, "");
 
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   unsigned char* v_op = k_op + (kCoded ? Sh::kOp : 0);
   unsigned char* q_op = smem + Sh::kOps;
   unsigned char* p_op = q_op + Sh::kQ;
-  unsigned char* slots = p_op + Sh::kP;                                   // .. and raw slots; bfloat16: operand slots
+  unsigned char* slots = p_op + Sh::kPs * Sh::kP;                                 // .. and raw slots; bfloat16: operand slots
   unsigned char* factors = slots + Sh::kSlots * Sh::kSlot + Sh::kPad;
   unsigned char* tops = factors + Sh::kFactors;
   unsigned char* misc = tops + Sh::kTops;
@@ -259,8 +260,10 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         tc::mbar_init(&bars->op_free[i], 1);
       }
       for (int i = 0; i < 2; ++i) tc::mbar_init(&bars->s_full[i], 1);
-      tc::mbar_init(&bars->p_full, 128 * Sh::kWGs);
-      tc::mbar_init(&bars->pv_done, 1);
+      tc::mbar_init(&bars->p_full[0], 128 * Sh::kWGs);
+      tc::mbar_init(&bars->p_full[1], 128 * Sh::kWGs);
+      tc::mbar_init(&bars->pv_done[0], 1);
+      tc::mbar_init(&bars->pv_done[1], 1);
       tc::mbar_init(&bars->drain, 1);
       tc::fence_mbar_init();
       *dead = 0;
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       for (int i = 0; i < n_tiles && ok; ++i) {
         if (i + 1 < n_tiles) ok = scores(i + 1);
         if (ok) ok = full(i, 1);
-        if (ok) ok = wait(&bars->p_full, i & 1, dead);
+        if (ok) ok = wait(&bars->p_full[i & 1], i / 2 & 1, dead);
         if (!ok) break;
         tc::fence_after_sync();
         const uint64_t v_desc = tc::smem_desc(operand(i, 1), Sh::kBlock, 1024, 2);
@@ -383,9 +386,9 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         for (int g = 0; g < Sh::kGroups; ++g)
 #pragma unroll
           for (int k = 0; k < TT / 16; ++k)
-            tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16, p_desc + k * (16 * N * 2) / 16,
+            tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16, p_desc + (i % Sh::kPs * Sh::kP + k * (16 * N * 2)) / 16,
                          kIdO, i > 0 || k > 0);
-        tc::mma_commit(&bars->pv_done);
+        tc::mma_commit(&bars->pv_done[i & 1]);
         release(i, 1);
       }
       if (!ok) {                                   // products in flight end before tensor memory is released
@@ -431,11 +434,6 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         for (int n = 0; n < R; ++n)
           if (absent || (node >= 0 && !(words[rows0 + n] >> node & 1))) x[n] = -INFINITY;
       }
-      if (i) {                                     // O is whole, and P's place free
-        ok &= wait(&bars->pv_done, (i - 1) & 1, dead);
-        ok = __all_sync(~0u, ok);
-        tc::fence_after_sync();
-      }
       float most = -INFINITY;
 #pragma unroll
       for (int n = 0; n < R; ++n) most = fmaxf(most, x[n]);
@@ -445,6 +443,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         for (int n = 0; n < R; ++n) move |= (unset >> n & 1) && x[n] > -INFINITY;
       }
       if (bar_or(bar, 128, move)) {
+        if (i) ok &= wait(&bars->pv_done[(i - 1) & 1], (i - 1) / 2 & 1, dead);   // O is whole
+        tc::fence_after_sync();
         if (bar_or(bar, 128, !ok)) break;
         // move the references: of the rows with such a score, to this tile's largest; of V's scales, to the largest
         float* mine = exchange + (wg * 4 + (warp & 3)) * 2 * R;
@@ -502,8 +502,10 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         l[n] += p0, l[n + 1] += p1;
         w[n / 2] = pack2<kCoded>(kCoded ? p0 * fold : p0, kCoded ? p1 * fold : p1);
       }
+      if (i >= Sh::kPs) ok = wait(&bars->pv_done[(i - Sh::kPs) & 1], (i - Sh::kPs) / 2 & 1, dead);   // P's place is free
+      ok = __all_sync(~0u, ok);
       // the token's rows, 16 bytes at a time; the swizzle xors their place with the address's bits 7 ..
-      unsigned char* p_at = p_op + tid * (N * 2);
+      unsigned char* p_at = p_op + i % Sh::kPs * Sh::kP + tid * (N * 2);
       const int turn = N == 16 ? tid >> 2 & 1 : (N == 32 ? tid >> 1 & 3 : tid & 7);
 #pragma unroll
       for (int y = 0; y < 2; ++y)
@@ -543,9 +545,9 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       }
       tc::fence_proxy_async();
       tc::fence_before_sync();
-      tc::mbar_arrive(&bars->p_full);
+      tc::mbar_arrive(&bars->p_full[i & 1]);
     }
-    if (ok) ok = wait(&bars->pv_done, (n_tiles - 1) & 1, dead);
+    if (ok) ok = wait(&bars->pv_done[(n_tiles - 1) & 1], (n_tiles - 1) / 2 & 1, dead);
     if (bar_or(5, 128 * Sh::kWGs, !ok || *dead)) {
       if (tid == 0) atomicCAS(a.status, 0u, (unsigned int)TACTKV_TIMEOUT);
     } else {
