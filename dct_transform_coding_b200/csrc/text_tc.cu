@@ -65,7 +65,7 @@ struct Shape {
   static constexpr int kCtas = N <= (kCoded ? 16 : 32) && kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot <= 113 * 1024 ? 2 : 1;
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;        // V operands in turn
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
-  static constexpr int kDecoders = !kCoded ? 0 : (N <= 32 && kCtas == 1 ? 16 : 8);
+  static constexpr int kDecoders = !kCoded ? 0 : (N <= 32 && kCtas == 1 && D > 64 ? 16 : 8);
   static constexpr int kThreads = 32 * (4 * kWGs + 2 + (kCoded ? kScalers + kDecoders : 0));
   static constexpr int kFit = ((kCtas == 2 ? 113 : 227) * 1024 - kRest - kOps) / kSlot;
   static constexpr int kSlots = kFit > kMaxSlots ? kMaxSlots : kFit;
@@ -83,6 +83,8 @@ struct Bars {
 static_assert(sizeof(Bars) <= 512, "");
 
 // False if the phase did not complete within kPolls, or if another wait of the block expired (dead, where given).
+// SLEEP: for waits with time to spare, whose polls would take issue slots from the warps that work.
+template <bool SLEEP = false>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
   const uint32_t a = tc::smem_u32(bar);
   for (uint32_t i = 0; i < kPolls; ++i) {
@@ -94,6 +96,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
         : "memory");
     if (done) return true;
     if (dead && (i & 15) == 15 && *dead) return false;
+    if constexpr (SLEEP) __nanosleep(50);
   }
   if (dead) *dead = 1;
   return false;
@@ -407,8 +410,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     uint32_t ref = 0, unset = (1u << R) - 1;       // rows that have seen no score yet (their reference is 0)
     bool ok = true;
     for (int i = 0; i < n_tiles; ++i) {
-      ok = wait(&bars->s_full[i & 1], i / 2 & 1, dead);
-      if constexpr (kCoded) ok &= wait(&bars->tops_full[i & 3], i / 4 & 1, dead);
+      ok = wait<kCoded>(&bars->s_full[i & 1], i / 2 & 1, dead);
+      if constexpr (kCoded) ok &= wait<true>(&bars->tops_full[i & 3], i / 4 & 1, dead);
       ok = __all_sync(~0u, ok);
       tc::fence_after_sync();
       const int t = t0 + i * TT + tid, node = t - before;
@@ -646,7 +649,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         int i, kv;
         tile_at(pos, i, kv);
         const int s = 2 * pos + half, slot = s % Sh::kSlots;
-        ok = __all_sync(~0u, wait(&bars->slot_full[slot], s / Sh::kSlots & 1, dead));
+        ok = __all_sync(~0u, wait<true>(&bars->slot_full[slot], s / Sh::kSlots & 1, dead));
         if (!ok) break;
         const int held = sp.len - (t0 + i * TT);
         const uint32_t bad = absent_of[i & 15];
@@ -698,63 +701,89 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     constexpr int kItems = Sh::kPart / 4 * Sh::kBlocks;                    // of eight lanes, in a slot
     constexpr int kPasses = (kItems + kAll / 8 - 1) / (kAll / 8);
     const int of = threadIdx.x - 32 * (kIssuer + 1 + kScalers), half = of / kAll, me = of % kAll;
+    // Where D is 64, 128 or 256 a lane's block, group and token modulo 8 are the same in every pass, and with them
+    // all of its offsets but for constants.
+    constexpr bool kSteady = kAll / 8 % Sh::kBlocks == 0;
+    constexpr int kStep = kAll / 8 / Sh::kBlocks * 4;                      // tokens from pass to pass
+    static_assert(!kSteady || (kStep % 8 == 0 && kItems % (kAll / 8) == 0), "");
+    struct Place {
+      int tok, g, raw, scale, out, chunk[4];
+    };
+    auto place_of = [&](int item) {
+      Place p;
+      const int block = item % Sh::kBlocks, sub = me % 2;
+      p.tok = item / Sh::kBlocks * 4 + me % 8 / 2;
+      p.g = block * 2 + sub;
+      p.raw = p.tok * Sh::kRow + p.g * (Sh::kRow / kGroupsRow);
+      p.scale = Sh::kRaw + p.tok * kGroupsRow + p.g;
+      p.out = block * Sh::kBlock + p.tok * 128;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) p.chunk[y] = ((sub * 4 + (FMT == kFp8 ? y ^ (p.tok & 1) * 2 : y)) ^ (p.tok & 7)) * 16;
+      return p;
+    };
+    // One group: its codes, scaled, to the operand.  Returns whether it may hold an infinity or NaN.
+    auto decode = [&](const unsigned char* raw, unsigned char* out, const Place& p, int pass, bool absent, bool look) {
+      const uint32_t f = reinterpret_cast<const uint32_t*>(factors)[raw[p.scale + pass * kStep * kGroupsRow]];
+      const unsigned char* from = raw + p.raw + pass * kStep * Sh::kRow;
+      unsigned char* to = out + p.out + pass * kStep * 128;
+      uint32_t odd = 0;
+      if constexpr (FMT == kFp8) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {              // the half that the lane takes first alternates with its token
+          uint4 w = *reinterpret_cast<const uint4*>(from + ((y ^ (p.tok & 1)) * 16));
+          if (absent) w = make_uint4(0, 0, 0, 0);
+          uint32_t h[8];
+          unpack_e4m3x4(w.x, h[0], h[1]);
+          unpack_e4m3x4(w.y, h[2], h[3]);
+          unpack_e4m3x4(w.z, h[4], h[5]);
+          unpack_e4m3x4(w.w, h[6], h[7]);
+#pragma unroll
+          for (int z = 0; z < 8; ++z) h[z] = mul_half2(h[z], f);
+          *reinterpret_cast<uint4*>(to + p.chunk[2 * y]) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(to + p.chunk[2 * y + 1]) = make_uint4(h[4], h[5], h[6], h[7]);
+          if (look) odd |= odd8(h);
+        }
+      } else {
+        uint4 w = *reinterpret_cast<const uint4*>(from);
+        if (absent) w = make_uint4(0, 0, 0, 0);
+        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t h[4];
+          unpack_e2m1x8(in[y], h);
+          *reinterpret_cast<uint4*>(to + p.chunk[y]) = make_uint4(mul_half2(h[0], f), mul_half2(h[1], f), mul_half2(h[2], f), mul_half2(h[3], f));
+        }
+        odd = (f & 0x7C00u) == 0x7C00u;            // E2M1 itself has no infinity or NaN
+      }
+      return odd != 0;
+    };
+    const Place mine = place_of(me / 8);
     bool ok = true;
     for (int pos = 0; pos < 2 * n_tiles && ok; ++pos) {
       int i, kv;
       tile_at(pos, i, kv);
       const int s = 2 * pos + half, slot = s % Sh::kSlots;
       const int op = kv ? 1 + i % Sh::kVOps : 0, turn = kv ? i / Sh::kVOps : i;
-      ok = wait(&bars->slot_scaled[slot], s / Sh::kSlots & 1, dead);
-      if (turn) ok &= wait(&bars->op_free[op], (turn - 1) & 1, dead);
+      ok = wait<true>(&bars->slot_scaled[slot], s / Sh::kSlots & 1, dead);
+      if (turn) ok &= wait<true>(&bars->op_free[op], (turn - 1) & 1, dead);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       const int t_half = t0 + i * TT + half * Sh::kPart, held = sp.len - t_half;
-      const uint32_t bad = absent_of[i & 15] >> (half * (Sh::kPart / 16));
-      const bool whole = held >= Sh::kPart && !(bad & ((1u << Sh::kPart / 16) - 1));
+      const uint32_t bad = absent_of[i & 15] >> (half * (Sh::kPart / 16)) & ((1u << Sh::kPart / 16) - 1);
       const unsigned char* raw = slots + slot * Sh::kSlot;
       unsigned char* out = k_op + op * Sh::kOp + half * Sh::kPart * 128;
+      const bool drafted = kv && t_half + Sh::kPart > before;
+      if (kSteady && held >= Sh::kPart && !bad && !drafted) {
 #pragma unroll
-      for (int pass = 0; pass < kPasses; ++pass) {
-        const int item = me / 8 + pass * (kAll / 8);
-        if (kItems % (kAll / 8) && item >= kItems) break;
-        const int block = item % Sh::kBlocks, tok = item / Sh::kBlocks * 4 + me % 8 / 2, g = block * 2 + me % 2;
-        const uint32_t f = reinterpret_cast<const uint32_t*>(factors)[raw[Sh::kRaw + tok * kGroupsRow + g]];
-        const bool absent = !whole && (tok >= held || (bad >> (tok / 16) & 1));
-        const bool drafted = kv && t_half + tok >= before;
-        uint32_t odd = 0;
-        unsigned char* to = out + block * Sh::kBlock + tok * 128;
-        const int chunk = me % 2 * 4;
-        if constexpr (FMT == kFp8) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int part = y ^ (tok & 1);
-            uint4 w = *reinterpret_cast<const uint4*>(raw + tok * Sh::kRow + g * 32 + part * 16);
-            if (absent) w = make_uint4(0, 0, 0, 0);
-            uint32_t h[8];
-            unpack_e4m3x4(w.x, h[0], h[1]);
-            unpack_e4m3x4(w.y, h[2], h[3]);
-            unpack_e4m3x4(w.z, h[4], h[5]);
-            unpack_e4m3x4(w.w, h[6], h[7]);
-#pragma unroll
-            for (int z = 0; z < 8; ++z) h[z] = mul_half2(h[z], f);
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-              *reinterpret_cast<uint4*>(to + ((chunk + part * 2 + z) ^ (tok & 7)) * 16) = make_uint4(h[4 * z], h[4 * z + 1], h[4 * z + 2], h[4 * z + 3]);
-            if (drafted) odd |= odd8(h);
-          }
-        } else {
-          uint4 w = *reinterpret_cast<const uint4*>(raw + tok * Sh::kRow + g * 16);
-          if (absent) w = make_uint4(0, 0, 0, 0);
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            uint32_t h[4];
-            unpack_e2m1x8(in[z], h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = mul_half2(h[e], f);
-            *reinterpret_cast<uint4*>(to + ((chunk + z) ^ (tok & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-          }
-          odd = drafted && (f & 0x7C00u) == 0x7C00u;   // E2M1 itself has no infinity or NaN
+        for (int pass = 0; pass < kPasses; ++pass) decode(raw, out, mine, pass, false, false);
+      } else {
+        bool odd = false;
+        for (int pass = 0; pass < kPasses; ++pass) {
+          const int item = me / 8 + pass * (kAll / 8);
+          if (item >= kItems) break;
+          const Place p = place_of(item);
+          const bool absent = p.tok >= held || (bad >> (p.tok / 16) & 1), look = drafted && t_half + p.tok >= before;
+          odd |= decode(raw, out, p, 0, absent, look) && look && !absent;
         }
         if (odd) *odd_tile = 1;
       }
