@@ -9,7 +9,6 @@
 //   softmax (4 or 8)  S^T from tensor memory -> P in shared memory; running maximum and sum in registers
 //   producer (1)      copies pages: TMA tiles into operand slots (bfloat16), bulk copies into raw slots (coded)
 //   issuer (1)        all products; the next tile's S^T is issued before this tile's O^T waits for its softmax
-//   scalers (2)       coded caches: each token's largest scale, and its groups' distances to it
 //   decoders (8, 16)  coded caches: raw slots -> half-precision operands, once for all rows of the unit
 // Every wait is bounded; one that expires records TACTKV_TIMEOUT and ends the block's work.
 //
@@ -35,7 +34,6 @@ namespace {
 constexpr int D = TACTKV_TEXT_D;
 constexpr int TT = 128;                           // tokens of a tile
 constexpr int kMaxSlots = 12;
-constexpr int kScalers = 2;                       // one for each half of a tile
 constexpr int R = 16;                             // rows of a softmax warpgroup
 constexpr float kToLog2 = to_log2(D);
 constexpr uint32_t kPolls = 1u << 16;             // of a wait; each suspends the thread for up to kPause ns
@@ -66,7 +64,7 @@ struct Shape {
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;        // V operands in turn
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
   static constexpr int kDecoders = !kCoded ? 0 : (N <= 32 && kCtas == 1 && D > 64 ? 16 : 8);
-  static constexpr int kThreads = 32 * (4 * kWGs + 2 + (kCoded ? kScalers + kDecoders : 0));
+  static constexpr int kThreads = 32 * (4 * kWGs + 2 + kDecoders);
   static constexpr int kFit = ((kCtas == 2 ? 113 : 227) * 1024 - kRest - kOps) / kSlot;
   static constexpr int kSlots = kFit > kMaxSlots ? kMaxSlots : kFit;
   static constexpr int kSmem = kRest + kOps + kSlots * kSlot;
@@ -77,7 +75,7 @@ struct Shape {
 };
 
 struct Bars {
-  uint64_t slot_full[kMaxSlots], slot_scaled[kMaxSlots], slot_free[kMaxSlots], op_full[3], op_free[3], tops_full[4],
+  uint64_t slot_full[kMaxSlots], slot_free[kMaxSlots], op_full[3], op_free[3], tops_full[4],
       s_full[2], p_full[2], pv_done[2], drain;
 };
 static_assert(sizeof(Bars) <= 512, "");
@@ -195,18 +193,18 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   if (row0 >= M || t0 >= sp.len) return;
   const int n_tiles = (min(sp.len - t0, parts.tokens) + TT - 1) / TT;
 
-  // K's tiles come one ahead of V's: K0 K1 V0 K2 V1 .. V(n-1).  Their places in that order:
-  auto place = [&](int i, int kv) { return !kv ? max(2 * i - 1, 0) : (i < n_tiles - 1 ? 2 * i + 2 : 2 * n_tiles - 1); };
-
-  auto tile_at = [&](int pos, int& i, int& kv) {   // and the other way
-    kv = pos == 2 * n_tiles - 1 || (pos && pos % 2 == 0);
-    i = kv ? (pos == 2 * n_tiles - 1 ? n_tiles - 1 : pos / 2 - 1) : (pos + 1) / 2;
-  };
+  // K's tiles are copied one ahead of V's: K0 K1 V0 K2 V1 .. V(n-1).  bfloat16 slots follow one another in that
+  // order.  Raw slots are rings of their own for K and V and for each half: a group of decoders sees every phase of its
+  // slots' barriers, and so can tell them apart.
+  constexpr int kRing = kCoded ? Sh::kSlots / 4 : Sh::kSlots;
+  auto turn_of = [&](int i, int kv) { return kCoded ? i : (!kv ? max(2 * i - 1, 0) : (i < n_tiles - 1 ? 2 * i + 2 : 2 * n_tiles - 1)); };
+  auto slot_of = [&](int i, int kv, int half) { return (kCoded ? (kv * 2 + half) * kRing : 0) + turn_of(i, kv) % kRing; };
+  auto round_of = [&](int i, int kv) { return turn_of(i, kv) / kRing; };
 
   // ---- the producer's copies ----
   const int page_tokens = 1 << a.c.page_log2, run = min(page_tokens, Sh::kPart), runs = TT / run, of_part = Sh::kPart / run;
   bool copies_ok = true;
-  int issued = 0;
+  int last_copy[2] = {-1, -1};                     // of K's and V's tiles
       long long at = 0, at_next = 0;                 // the lane's run of this V's and the next K's tile
       uint32_t good = 0, good_next = 0;              // the lanes whose runs are there
       auto find = [&](int i) {                       // a lane copies a run of tokens, which never leaves its page
@@ -220,17 +218,17 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         good_next = __ballot_sync(~0u, in);
         at_next = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & (page_tokens - 1));
       };
-      auto copy = [&](int kv, int pos) {
+      auto copy = [&](int kv, int i) {
         const long long from = kv ? at : at_next;
         const uint32_t mask = kv ? good : good_next;
         for (int half = 0; half < Sh::kParts && copies_ok; ++half) {
-          const int s = Sh::kParts * pos + half, slot = s % Sh::kSlots, round = s / Sh::kSlots;
+          const int slot = slot_of(i, kv, half), round = round_of(i, kv);
           if (round) copies_ok = wait(&bars->slot_free[slot], (round - 1) & 1, dead);
           copies_ok = __all_sync(~0u, copies_ok);
           if (!copies_ok) break;
           const int mine = __popc(mask >> (half * of_part) & ((2u << (of_part - 1)) - 1));
           if (lane == 0) tc::mbar_expect_tx(&bars->slot_full[slot], mine * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
-          issued = s + 1;
+          last_copy[kv] = i;
           __syncwarp();
           if ((mask >> lane & 1) && lane / of_part == half) {
             unsigned char* to = slots + slot * Sh::kSlot;
@@ -254,12 +252,11 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     if (lane == 0) {
       for (int i = 0; i < Sh::kSlots; ++i) {
         tc::mbar_init(&bars->slot_full[i], 1);
-        tc::mbar_init(&bars->slot_scaled[i], 1);
-        tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders / 2 : 1);
+        tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders / 4 : 1);
       }
-      for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->tops_full[i], kScalers);
+      for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->tops_full[i], 2);
       for (int i = 0; i < 3; ++i) {                // K's operand, V's (one or two)
-        tc::mbar_init(&bars->op_full[i], kCoded ? Sh::kDecoders : 1);
+        tc::mbar_init(&bars->op_full[i], kCoded ? Sh::kDecoders / 2 : 1);
         tc::mbar_init(&bars->op_free[i], 1);
       }
       for (int i = 0; i < 2; ++i) tc::mbar_init(&bars->s_full[i], 1);
@@ -338,13 +335,15 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       at = at_next, good = good_next;
       if (i + 1 < n_tiles) {
         find(i + 1);
-        copy(0, place(i + 1, 0));
+        copy(0, i + 1);
       }
-      if (copies_ok) copy(1, place(i, 1));
+      if (copies_ok) copy(1, i);
     }
     // Copies in flight when a wait expired land before the block ends.
     if (!copies_ok)
-      for (int s = max(0, issued - Sh::kSlots); s < issued; ++s) wait(&bars->slot_full[s % Sh::kSlots], s / Sh::kSlots & 1, nullptr);
+      for (int kv = 0; kv < 2; ++kv)
+        for (int i = max(0, last_copy[kv] - kRing + 1); i <= last_copy[kv]; ++i)
+          for (int half = 0; half < Sh::kParts; ++half) wait(&bars->slot_full[slot_of(i, kv, half)], round_of(i, kv) & 1, nullptr);
   } else if (warp == kIssuer) {
     // -------------------------------------------------------------------------------- issuer ---
     if (lane == 0) {
@@ -355,14 +354,14 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       const uint32_t q_addr = tc::smem_u32(q_op), p_addr = tc::smem_u32(p_op);
       auto op = [&](int i, int kv) { return kv ? 1 + i % Sh::kVOps : 0; };
       auto operand = [&](int i, int kv) {
-        return tc::smem_u32(kCoded ? k_op + op(i, kv) * Sh::kOp : slots + place(i, kv) % Sh::kSlots * Sh::kSlot);
+        return tc::smem_u32(kCoded ? k_op + op(i, kv) * Sh::kOp : slots + slot_of(i, kv, 0) * Sh::kSlot);
       };
       auto full = [&](int i, int kv) {
         return kCoded ? wait(&bars->op_full[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, dead)
-                      : wait(&bars->slot_full[place(i, kv) % Sh::kSlots], place(i, kv) / Sh::kSlots & 1, dead);
+                      : wait(&bars->slot_full[slot_of(i, kv, 0)], round_of(i, kv) & 1, dead);
       };
       auto release = [&](int i, int kv) {
-        tc::mma_commit(kCoded ? &bars->op_free[op(i, kv)] : &bars->slot_free[place(i, kv) % Sh::kSlots]);
+        tc::mma_commit(kCoded ? &bars->op_free[op(i, kv)] : &bars->slot_free[slot_of(i, kv, 0)]);
       };
       const uint64_t q_desc = tc::smem_desc(q_addr, 16, 1024, 2), p_desc = tc::smem_desc(p_addr, 16, 8 * N * 2, kSwizzle);
       auto scores = [&](int i) {
@@ -516,10 +515,12 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       // Behind the last token V's operand holds whatever the page holds (decoders write zeros there), and a
       // drafted token's infinities and NaN are for some rows only: zeros take their place.
       if (wg == 0 && (tail || (bad && !kCoded))) {
-        ok = wait(kCoded ? &bars->op_full[1 + i % Sh::kVOps] : &bars->slot_full[place(i, 1) % Sh::kSlots],
-                  (kCoded ? i / Sh::kVOps : place(i, 1) / Sh::kSlots) & 1, dead);
+        // (The operand's barrier is in this tile's phase, or the one before, only when the last tile's is used.)
+        if (i) ok &= wait(&bars->pv_done[(i - 1) & 1], (i - 1) / 2 & 1, dead);
+        ok &= wait(kCoded ? &bars->op_full[1 + i % Sh::kVOps] : &bars->slot_full[slot_of(i, 1, 0)],
+                   (kCoded ? i / Sh::kVOps : round_of(i, 1)) & 1, dead);
         ok = __all_sync(~0u, ok);
-        unsigned char* v = kCoded ? v_op + i % Sh::kVOps * Sh::kOp : slots + place(i, 1) % Sh::kSlots * Sh::kSlot;
+        unsigned char* v = kCoded ? v_op + i % Sh::kVOps * Sh::kOp : slots + slot_of(i, 1, 0) * Sh::kSlot;
         const int base = t0 + i * TT, held = min(sp.len - base, TT);
         if (!kCoded) {
           const int from = bad ? 0 : held;
@@ -637,70 +638,15 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       }
     }
     tc::fence_before_sync();
-  } else if (kCoded && warp <= kIssuer + kScalers) {
-    // -------------------------------------------------------------------------------- scaler ---
-    // A lane takes a token: the largest of its scales (the NaN scale aside), and in the scales' place every
-    // group's distance to it (31: 2^-25 and less are 0 in half precision; 63: NaN).
-    if constexpr (kCoded) {
-      constexpr int kGroupsRow = D / kGroup;
-      bool ok = true;
-      const int half = warp - kIssuer - 1;
-      for (int pos = 0; pos < 2 * n_tiles && ok; ++pos) {
-        int i, kv;
-        tile_at(pos, i, kv);
-        const int s = 2 * pos + half, slot = s % Sh::kSlots;
-        ok = __all_sync(~0u, wait<true>(&bars->slot_full[slot], s / Sh::kSlots & 1, dead));
-        if (!ok) break;
-        const int held = sp.len - (t0 + i * TT);
-        const uint32_t bad = absent_of[i & 15];
-#pragma unroll
-        for (int x = 0; x < Sh::kPart / 32; ++x) {
-          const int in = 32 * x + lane, tok = half * Sh::kPart + in;
-          const bool absent = tok >= held || (bad >> (tok / 16) & 1);
-          unsigned char* sc = slots + slot * Sh::kSlot + Sh::kRaw + in * kGroupsRow;
-          uint32_t b[kGroupsRow], top = 0;
-          if constexpr (kGroupsRow % 4 == 0) {
-#pragma unroll
-            for (int g = 0; g < kGroupsRow; g += 4) {
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + g);
-              b[g] = w & 255u, b[g + 1] = w >> 8 & 255u, b[g + 2] = w >> 16 & 255u, b[g + 3] = w >> 24;
-            }
-          } else {
-#pragma unroll
-            for (int g = 0; g < kGroupsRow; ++g) b[g] = sc[g];
-          }
-#pragma unroll
-          for (int g = 0; g < kGroupsRow; ++g) top = max(top, b[g] == 255u ? 0u : b[g]);
-          if (absent) top = 0;
-          tops[((i & 3) * 2 + kv) * TT + tok] = (unsigned char)top;
-#pragma unroll
-          for (int g = 0; g < kGroupsRow; ++g) b[g] = absent ? 0u : (b[g] == 255u ? 63u : min(top - min(b[g], top), 31u));
-          if constexpr (kGroupsRow % 4 == 0) {
-#pragma unroll
-            for (int g = 0; g < kGroupsRow; g += 4)
-              *reinterpret_cast<uint32_t*>(sc + g) = b[g] | b[g + 1] << 8 | b[g + 2] << 16 | b[g + 3] << 24;
-          } else {
-#pragma unroll
-            for (int g = 0; g < kGroupsRow; ++g) sc[g] = (unsigned char)b[g];
-          }
-        }
-        tc::fence_proxy_async();                   // the next copy into the slot comes after these stores
-        __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&bars->slot_scaled[slot]);
-          if (kv) tc::mbar_arrive(&bars->tops_full[i & 3]);
-        }
-      }
-    }
   } else if constexpr (kCoded) {
     // ------------------------------------------------------------------------------ decoders ---
     // A lane takes a group of 32 values at a time.  Eight lanes take four tokens' two groups of a 64-column block, and
     // odd tokens their halves in the other order, so that stores of 16 bytes never meet in a bank.
-    // Half of the decoders take a tile's first 64 tokens, the others the rest.
-    constexpr int kAll = 16 * Sh::kDecoders, kGroupsRow = D / kGroup;
+    // Four groups: for K and for V, for a tile's first 64 tokens and for the rest.
+    constexpr int kAll = 8 * Sh::kDecoders, kGroupsRow = D / kGroup;
     constexpr int kItems = Sh::kPart / 4 * Sh::kBlocks;                    // of eight lanes, in a slot
     constexpr int kPasses = (kItems + kAll / 8 - 1) / (kAll / 8);
-    const int of = threadIdx.x - 32 * (kIssuer + 1 + kScalers), half = of / kAll, me = of % kAll;
+    const int of = threadIdx.x - 32 * (kIssuer + 1), kv = of / kAll / 2, half = of / kAll % 2, me = of % kAll;
     // Where D is 64, 128 or 256 a lane's block, group and token modulo 8 are the same in every pass, and with them
     // all of its offsets but for constants.
     constexpr bool kSteady = kAll / 8 % Sh::kBlocks == 0;
@@ -759,17 +705,48 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     };
     const Place mine = place_of(me / 8);
     bool ok = true;
-    for (int pos = 0; pos < 2 * n_tiles && ok; ++pos) {
-      int i, kv;
-      tile_at(pos, i, kv);
-      const int s = 2 * pos + half, slot = s % Sh::kSlots;
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      const int slot = slot_of(i, kv, half);
       const int op = kv ? 1 + i % Sh::kVOps : 0, turn = kv ? i / Sh::kVOps : i;
-      ok = wait<true>(&bars->slot_scaled[slot], s / Sh::kSlots & 1, dead);
-      if (turn) ok &= wait<true>(&bars->op_free[op], (turn - 1) & 1, dead);
+      const int t_half = t0 + i * TT + half * Sh::kPart, held = sp.len - t_half;
+      ok = __all_sync(~0u, wait<true>(&bars->slot_full[slot], round_of(i, kv) & 1, dead));
+      const uint32_t bad = absent_of[i & 15] >> (half * (Sh::kPart / 16)) & ((1u << Sh::kPart / 16) - 1);
+      // One lane to a token: the largest of its scales (the NaN scale aside), and in the scales' place every group's
+      // distance to it (31: 2^-25 and less are 0 in half precision; 63: NaN).
+      if (ok && me < Sh::kPart) {
+        const bool absent = me >= held || (bad >> (me / 16) & 1);
+        unsigned char* sc = slots + slot * Sh::kSlot + Sh::kRaw + me * kGroupsRow;
+        uint32_t b[kGroupsRow], top = 0;
+        if constexpr (kGroupsRow % 4 == 0) {
+#pragma unroll
+          for (int g = 0; g < kGroupsRow; g += 4) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + g);
+            b[g] = w & 255u, b[g + 1] = w >> 8 & 255u, b[g + 2] = w >> 16 & 255u, b[g + 3] = w >> 24;
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < kGroupsRow; ++g) b[g] = sc[g];
+        }
+#pragma unroll
+        for (int g = 0; g < kGroupsRow; ++g) top = max(top, b[g] == 255u ? 0u : b[g]);
+        if (absent) top = 0;
+        tops[((i & 3) * 2 + kv) * TT + half * Sh::kPart + me] = (unsigned char)top;
+#pragma unroll
+        for (int g = 0; g < kGroupsRow; ++g) b[g] = absent ? 0u : (b[g] == 255u ? 63u : min(top - min(b[g], top), 31u));
+        if constexpr (kGroupsRow % 4 == 0) {
+#pragma unroll
+          for (int g = 0; g < kGroupsRow; g += 4)
+            *reinterpret_cast<uint32_t*>(sc + g) = b[g] | b[g + 1] << 8 | b[g + 2] << 16 | b[g + 3] << 24;
+        } else {
+#pragma unroll
+          for (int g = 0; g < kGroupsRow; ++g) sc[g] = (unsigned char)b[g];
+        }
+      }
+      if (bar_or(6 + 2 * kv + half, kAll, !ok)) break;
+      if (kv && me == 0) tc::mbar_arrive(&bars->tops_full[i & 3]);
+      if (turn) ok = wait<true>(&bars->op_free[op], (turn - 1) & 1, dead);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
-      const int t_half = t0 + i * TT + half * Sh::kPart, held = sp.len - t_half;
-      const uint32_t bad = absent_of[i & 15] >> (half * (Sh::kPart / 16)) & ((1u << Sh::kPart / 16) - 1);
       const unsigned char* raw = slots + slot * Sh::kSlot;
       unsigned char* out = k_op + op * Sh::kOp + half * Sh::kPart * 128;
       const bool drafted = kv && t_half + Sh::kPart > before;
