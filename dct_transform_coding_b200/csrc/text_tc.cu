@@ -458,38 +458,52 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         const uint32_t top = __reduce_max_sync(~0u, v_top);
         if (lane == 0) mine[R] = __uint_as_float(top);
         bar_sync(bar);
-        const float* all = exchange + wg * 4 * 2 * R;
+        float* all = exchange + wg * 4 * 2 * R;
         uint32_t new_ref = ref;
 #pragma unroll
         for (int w = 0; w < 4; ++w) new_ref = max(new_ref, __float_as_uint(all[w * 2 * R + R]));
+        float shift = 0.f, scale = 1.f;            // of row rows0 + tid
+        if (tid < 32) {
+          bool moves = false;
+          if (tid < R) {
+            const float by = fmaxf(fmaxf(all[tid], all[2 * R + tid]), fmaxf(all[4 * R + tid], all[6 * R + tid]));
+            const bool first = unset >> tid & 1;
+            moves = by > (first ? -INFINITY : kSlack);
+            if (moves) {
+              shift = by;
+              scale = first ? 0.f : exp2_fast(-by);
+              row_fm[rows0 + tid].y -= by;
+            }
+          }
+          const uint32_t moved = __ballot_sync(~0u, moves);
+          if (tid == 0) all[4 * R + R + 1] = __uint_as_float(moved);
+        }
+        bar_sync(bar);                             // the exchanged maxima are read
+        if (tid < R) all[tid] = shift, all[2 * R + tid] = scale;
+        bar_sync(bar);
+        const uint32_t moved = __float_as_uint(all[4 * R + R + 1]);
         const float down = kCoded ? __uint_as_float((uint32_t)max(127 + (int)ref - (int)new_ref, 0) << 23) : 1.f;
         ref = new_ref;
-        float keep[R];
+        unset &= ~moved;
 #pragma unroll
         for (int n = 0; n < R; ++n) {
-          const float by = fmaxf(fmaxf(all[n], all[2 * R + n]), fmaxf(all[4 * R + n], all[6 * R + n]));
-          const bool first = unset >> n & 1;
-          keep[n] = 1.f;
-          if (by > (first ? -INFINITY : kSlack)) {
-            x[n] -= by;
-            keep[n] = first ? 0.f : exp2_fast(-by);
-            l[n] *= keep[n];
-            high[n] = -INFINITY;                   // all before is below this tile's largest
-            unset &= ~(1u << n);
-            if (tid == n) row_fm[rows0 + n].y -= by;
-          }
-          keep[n] *= down;
+          x[n] -= all[n];
+          l[n] *= all[2 * R + n];
+          if (moved >> n & 1) high[n] = -INFINITY;  // all before is below this tile's largest
         }
         if (i) {
-#pragma unroll
+#pragma unroll 1
           for (int g = 0; g < Sh::kGroups; ++g) {
-            const uint32_t at = lanes + (2 + g) * N + rows0;
-            float v[R];
-            tc::tmem_ld<R>(at, v);
-            tc::tmem_ld_wait();
+#pragma unroll 1
+            for (int c = 0; c < R; c += 8) {
+              const uint32_t at = lanes + (2 + g) * N + rows0 + c;
+              float v[8];
+              tc::tmem_ld<8>(at, v);
+              tc::tmem_ld_wait();
 #pragma unroll
-            for (int n = 0; n < R; ++n) v[n] *= keep[n];
-            tc::tmem_st16(at, v);
+              for (int n = 0; n < 8; ++n) v[n] *= all[2 * R + c + n] * down;
+              tc::tmem_st8(at, v);
+            }
           }
           tc::tmem_st_wait();
         }
