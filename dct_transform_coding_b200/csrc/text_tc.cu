@@ -63,7 +63,7 @@ struct Shape {
   static constexpr int kCtas = N <= (kCoded ? 16 : 32) && kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot <= 113 * 1024 ? 2 : 1;
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;        // V operands in turn
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
-  static constexpr int kDecoders = !kCoded ? 0 : (N <= 32 && kCtas == 1 && D > 64 ? 16 : 8);
+  static constexpr int kDecoders = !kCoded ? 0 : (D > 128 ? 16 : 8);
   static constexpr int kThreads = 32 * (4 * kWGs + 2 + kDecoders);
   static constexpr int kFit = ((kCtas == 2 ? 113 : 227) * 1024 - kRest - kOps) / kSlot;
   static constexpr int kSlots = kFit > kMaxSlots ? kMaxSlots : kFit;
@@ -154,7 +154,7 @@ __device__ __forceinline__ float reduce_rows(float (&v)[R]) {
 
 template <int FMT, int N>
 __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
-    tc_kernel(const AttnArgs a, const Parts parts, const __grid_constant__ CUtensorMap k_map,
+    tc_kernel(const AttnArgs a, const Flat flat, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<FMT, N>;
   constexpr bool kCoded = Sh::kCoded;
@@ -181,17 +181,27 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = a.q_heads / a.c.heads;
-  const int part = blockIdx.x, seq = blockIdx.z, tiles = gridDim.y / a.c.heads;
-  const int head = blockIdx.y / tiles, tile = blockIdx.y % tiles;
-  const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
-  if (!sp.ok) {                                   // the sequence's rows see no text token
-    if (part == 0 && tile == 0) finish_misfit<false, D>(a, sp, seq, head, G);
-    return;
+  constexpr int kProducer = 4 * Sh::kWGs, kIssuer = kProducer + 1;
+  for (int seq = blockIdx.x; seq < a.b.n_seqs; seq += gridDim.x) {
+    const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
+    if (!sp.ok)
+      for (int head = 0; head < a.c.heads; ++head) finish_misfit<false, D>(a, sp, seq, head, G);
   }
-  const int M = sp.rows * G, row0 = tile * N, before = sp.len - sp.rows;
-  const int t0 = part * parts.tokens;
-  if (row0 >= M || t0 >= sp.len) return;
-  const int n_tiles = (min(sp.len - t0, parts.tokens) + TT - 1) / TT;
+  Piece piece;
+  const long long entries = find_entry(a, N, flat.whole, -1, &piece);
+  const long long share = max((entries + gridDim.x - 1) / gridDim.x, (long long)(flat.whole ? 1 : kLeastShare));
+  const long long end = min(entries, (blockIdx.x + 1) * share);
+  if (blockIdx.x * share >= end) return;
+  if (warp == kIssuer) tc::tmem_alloc(tmem_slot, Sh::kTmem);
+  bool done = false;
+  for (long long at_entry = blockIdx.x * share; at_entry < end && !done;) {
+  const bool first_piece = at_entry == blockIdx.x * share;
+  find_entry(a, N, flat.whole, at_entry, &piece);
+  const Span& sp = piece.sp;
+  const int seq = piece.seq, head = piece.head;
+  const int M = sp.rows * G, row0 = piece.tile * N, before = sp.len - sp.rows;
+  const int t0 = piece.first * TT, n_tiles = flat.whole ? piece.of : (int)min((long long)piece.tiles, end - at_entry);
+  at_entry += flat.whole ? 1 : n_tiles;
 
   // K's tiles are copied one ahead of V's: K0 K1 V0 K2 V1 .. V(n-1).  bfloat16 slots follow one another in that
   // order.  Raw slots are rings of their own for K and V and for each half: a group of decoders sees every phase of its
@@ -247,10 +257,11 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       };
 
   // ---- set up: barriers and the first copy, tensor memory, the queries' operand ----
-  constexpr int kProducer = 4 * Sh::kWGs, kIssuer = kProducer + 1;
   if (warp == kProducer) {
     if (lane == 0) {
-      for (int i = 0; i < Sh::kSlots; ++i) {
+      if (!first_piece)
+        for (int i = 0; i < (int)(sizeof(Bars) / 8); ++i) tc::mbar_inval(reinterpret_cast<uint64_t*>(bars) + i);
+      for (int i = 0; i < kMaxSlots; ++i) {
         tc::mbar_init(&bars->slot_full[i], 1);
         tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders / 4 : 1);
       }
@@ -266,16 +277,14 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       tc::mbar_init(&bars->pv_done[1], 1);
       tc::mbar_init(&bars->drain, 1);
       tc::fence_mbar_init();
-      *dead = 0;
+      if (first_piece) *dead = 0;
       odd_nodes[0] = odd_nodes[1] = 0;
       *odd_tile = 0;
     }
     __syncwarp();
     find(0);
     copy(0, 0);
-  } else if (warp == kIssuer) {
-    tc::tmem_alloc(tmem_slot, Sh::kTmem);
-  } else {
+  } else if (warp != kIssuer) {
     constexpr int E = D / 32, kStagers = Sh::kThreads / 32 - 2, kMine = (N + kStagers - 1) / kStagers;
     const int stager = warp < kProducer ? warp : warp - 2;
     uint32_t w[kMine][E / 2];                      // a warp per row, lane i with its elements i * E ..; all rows' loads first
@@ -393,9 +402,13 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         tc::mma_commit(&bars->pv_done[i & 1]);
         release(i, 1);
       }
-      if (!ok) {                                   // products in flight end before tensor memory is released
-        tc::mma_commit(&bars->drain);
-        wait(&bars->drain, 0, nullptr);
+      // Every product and every arrival is in before the barriers and tensor memory are used anew.
+      tc::mma_commit(&bars->drain);
+      wait(&bars->drain, 0, nullptr);
+      for (int kv = 0; kv < 2 && ok; ++kv) {
+        const int i = n_tiles - 1;
+        if (kCoded) wait(&bars->op_free[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, nullptr);
+        else wait(&bars->slot_free[slot_of(i, kv, 0)], round_of(i, kv) & 1, nullptr);
       }
     }
     __syncwarp();
@@ -636,21 +649,22 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (row < M) {
         const float2 ml = row_ml[n];
         const float* from = sums + n * (D + 4) + tid % 8 * 4;
-        if (parts.count == 1) {
+        if (n_tiles == piece.of) {
           const long long at = (long long)(sp.first + row / G) * a.q_heads + head * G + row % G;
           const RowEnd e = end_row(a, at, ml.x, ml.y, tid % 8 == 0);
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
             finish4<false>(a, at, tid % 8 * 4 + 32 * k, *reinterpret_cast<const float4*>(from + 32 * k), e);
         } else {
-          const long long to = ((long long)part * gridDim.z * gridDim.y + seq * gridDim.y + blockIdx.y) * N + n;
+          const long long to = (2ll * blockIdx.x + !first_piece) * N + n;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            *reinterpret_cast<float4*>(parts.o + to * D + tid % 8 * 4 + 32 * k) = *reinterpret_cast<const float4*>(from + 32 * k);
-          if (tid % 8 == 0) parts.ml[to] = ml;
+            *reinterpret_cast<float4*>(flat.o + to * D + tid % 8 * 4 + 32 * k) = *reinterpret_cast<const float4*>(from + 32 * k);
+          if (tid % 8 == 0) flat.ml[to] = ml;
         }
       }
     }
+    tc::fence_proxy_async();                       // the next piece's copies come after these stores
     tc::fence_before_sync();
   } else if constexpr (kCoded) {
     // ------------------------------------------------------------------------------ decoders ---
@@ -787,10 +801,10 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     }
   }
   __syncthreads();
-  if (warp == kIssuer) {
-    tc::fence_after_sync();
-    tc::tmem_free(tmem, Sh::kTmem);
+  tc::fence_after_sync();
+  done = *dead;
   }
+  if (warp == kIssuer) tc::tmem_free(*tmem_slot, Sh::kTmem);
 }
 
 bool make_map(const AttnArgs& a, int kv, CUtensorMap* map) {
@@ -813,7 +827,7 @@ bool make_map(const AttnArgs& a, int kv, CUtensorMap* map) {
 }
 
 template <int FMT, int N>
-cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, Flat f, int rows, cudaStream_t st) {
   using Sh = Shape<FMT, N>;
   // the kernel's shared memory is set once for each device (twice by two threads at once does no harm)
   static std::atomic<unsigned long long> set{0};
@@ -827,14 +841,20 @@ cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
   }
   CUtensorMap maps[2] = {};
   if (FMT == kBf16 && !(make_map(a, 0, &maps[0]) && make_map(a, 1, &maps[1]))) return cudaErrorInvalidValue;
-  tc_kernel<FMT, N><<<dim3(p.count, a.c.heads * p.tiles, a.b.n_seqs), Sh::kThreads, Sh::kSmem, st>>>(a, p, maps[0], maps[1]);
-  return cudaGetLastError();
+  f.rows = N;
+  const long long units = (long long)a.b.n_seqs * a.c.heads * ((rows + N - 1) / N), tiles = (a.max_len + TT - 1) / TT;
+  f.whole = tiles <= kLeastShare;
+  const long long most = f.whole ? units : std::max(units * tiles / kLeastShare, 1ll);
+  const int blocks = (int)std::min(most, (long long)kSms * Sh::kCtas);
+  tc_kernel<FMT, N><<<blocks, Sh::kThreads, Sh::kSmem, st>>>(a, f, maps[0], maps[1]);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess || f.whole || blocks == 1 ? e : launch_flat_combine(a, f, blocks, st);
 }
 template <int FMT>
-cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
-  if (p.tile_rows == 16) return launch<FMT, 16>(a, p, st);
-  if (p.tile_rows == 32) return launch<FMT, 32>(a, p, st);
-  if constexpr (D <= kWideDim) return launch<FMT, 64>(a, p, st);
+cudaError_t launch(const AttnArgs& a, const Flat& f, int rows, cudaStream_t st) {
+  if (rows <= 16) return launch<FMT, 16>(a, f, rows, st);
+  if (rows <= 32 || D > kWideDim) return launch<FMT, 32>(a, f, rows, st);
+  if constexpr (D <= kWideDim) return launch<FMT, 64>(a, f, rows, st);
   return cudaErrorInvalidValue;
 }
 
@@ -842,8 +862,8 @@ cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
 
 #define TACTKV_CAT_(x, y) x##y
 #define TACTKV_CAT(x, y) TACTKV_CAT_(x, y)
-cudaError_t TACTKV_CAT(launch_tc_, TACTKV_TEXT_D)(int fmt, const AttnArgs& a, const Parts& p, cudaStream_t st) {
-  return fmt == kBf16 ? launch<kBf16>(a, p, st) : (fmt == kFp8 ? launch<kFp8>(a, p, st) : launch<kFp4>(a, p, st));
+cudaError_t TACTKV_CAT(launch_tc_, TACTKV_TEXT_D)(int fmt, const AttnArgs& a, const Flat& f, int rows, cudaStream_t st) {
+  return fmt == kBf16 ? launch<kBf16>(a, f, rows, st) : (fmt == kFp8 ? launch<kFp8>(a, f, rows, st) : launch<kFp4>(a, f, rows, st));
 }
 
 }  // namespace text
