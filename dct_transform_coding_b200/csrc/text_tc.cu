@@ -74,6 +74,11 @@ struct Shape {
   static_assert(N * (D + 4) * 4 <= kOps + (kCoded ? 0 : kSlots * kSlot), "the sums take the operands' place");
 };
 
+struct Job {            // a piece: part or all of a unit's tokens
+  long long next, end, after;                     // entries of the list: where this piece begins, the share's end, where the next begins
+  int number, seq, head, tile, first, tiles, of, row, rows, len;
+};
+
 struct Bars {
   uint64_t slot_full[kMaxSlots], slot_free[kMaxSlots], op_full[3], op_free[3], tops_full[4],
       s_full[2], p_full[2], pv_done[2], drain;
@@ -187,21 +192,34 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     if (!sp.ok)
       for (int head = 0; head < a.c.heads; ++head) finish_misfit<false, D>(a, sp, seq, head, G);
   }
-  Piece piece;
-  const long long entries = find_entry(a, N, flat.whole, -1, &piece);
-  const long long share = max((entries + gridDim.x - 1) / gridDim.x, (long long)(flat.whole ? 1 : kLeastShare));
-  const long long end = min(entries, (blockIdx.x + 1) * share);
-  if (blockIdx.x * share >= end) return;
+  // The block's share of the list.  Its pieces are found by one warp and passed on in shared memory.
+  volatile Job* job = reinterpret_cast<Job*>(misc + 640);
+  if (warp == 0) {
+    const long long entries = find_entry(a, N, flat.whole, -1, nullptr);
+    const long long share = max((entries + gridDim.x - 1) / gridDim.x, (long long)(flat.whole ? 1 : kLeastShare));
+    if (lane == 0) job->next = blockIdx.x * share, job->end = min(entries, (blockIdx.x + 1) * share), job->number = -1;
+  }
   if (warp == kIssuer) tc::tmem_alloc(tmem_slot, Sh::kTmem);
-  bool done = false;
-  for (long long at_entry = blockIdx.x * share; at_entry < end && !done;) {
-  const bool first_piece = at_entry == blockIdx.x * share;
-  find_entry(a, N, flat.whole, at_entry, &piece);
-  const Span& sp = piece.sp;
-  const int seq = piece.seq, head = piece.head;
-  const int M = sp.rows * G, row0 = piece.tile * N, before = sp.len - sp.rows;
-  const int t0 = piece.first * TT, n_tiles = flat.whole ? piece.of : (int)min((long long)piece.tiles, end - at_entry);
-  at_entry += flat.whole ? 1 : n_tiles;
+  __syncthreads();
+  while (job->next < job->end) {
+  if (warp == 0) {
+    Piece p;
+    const long long next = job->next;
+    find_entry(a, N, flat.whole, next, &p);
+    __syncwarp();
+    if (lane == 0) {
+      const int n = flat.whole ? p.of : (int)min((long long)p.tiles, job->end - next);
+      job->seq = p.seq, job->head = p.head, job->tile = p.tile, job->first = p.first, job->tiles = n, job->of = p.of;
+      job->row = p.sp.first, job->rows = p.sp.rows, job->len = p.sp.len, job->number = job->number + 1;
+      job->after = next + (flat.whole ? 1 : n);
+    }
+  }
+  __syncthreads();
+  const bool first_piece = job->number == 0;
+  const Span sp = {job->row, job->rows, job->len, true};
+  const int seq = job->seq, head = job->head;
+  const int M = sp.rows * G, row0 = job->tile * N, before = sp.len - sp.rows;
+  const int t0 = job->first * TT, n_tiles = job->tiles;
 
   // K's tiles are copied one ahead of V's: K0 K1 V0 K2 V1 .. V(n-1).  bfloat16 slots follow one another in that
   // order.  Raw slots are rings of their own for K and V and for each half: a group of decoders sees every phase of its
@@ -649,7 +667,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (row < M) {
         const float2 ml = row_ml[n];
         const float* from = sums + n * (D + 4) + tid % 8 * 4;
-        if (n_tiles == piece.of) {
+        if (n_tiles == job->of) {
           const long long at = (long long)(sp.first + row / G) * a.q_heads + head * G + row % G;
           const RowEnd e = end_row(a, at, ml.x, ml.y, tid % 8 == 0);
 #pragma unroll
@@ -802,7 +820,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   }
   __syncthreads();
   tc::fence_after_sync();
-  done = *dead;
+  if (threadIdx.x == 0) job->next = *dead ? job->end : job->after;
+  __syncthreads();
   }
   if (warp == kIssuer) tc::tmem_free(*tmem_slot, Sh::kTmem);
 }
