@@ -17,19 +17,9 @@ constexpr int kMaxParts = 4 * 148; // units times parts, where there is more tha
 constexpr int kLeastPart = 256;    // tokens
 constexpr int kWideDim = 128;      // up to this head_dim a unit may have 32 rows (registers for their sums)
 
-constexpr int kSms = 148;
-// Of text_tc.cu's kernel: a block's partial results are its first piece's and its last's.
-constexpr int kLeastShare = 2;     // entries
-struct Flat {
-  int rows;            // 16, 32 or 64
-  bool whole;          // an entry is a whole unit: nothing is split
-  float* o;            // [block][2][rows][D]
-  float2* ml;          // [block][2][rows]
-};
-
 constexpr int kPartRows(int D) { return D <= kWideDim ? 64 : 32; }
 
-// Of text_attention.cu's kernel.  A unit is (sequence, K/V head, tile of tile_rows rows), numbered in that order.
+// A unit is (sequence, K/V head, tile of tile_rows rows), numbered in that order.
 struct Parts {
   int tile_rows;       // 8, 16 or 32
   int tiles;           // for max_rows * G rows
@@ -135,55 +125,6 @@ __device__ __forceinline__ void finish4(const AttnArgs& a, long long at, int d, 
   finish4<F32>(a, at, d, o, end_row(a, at, m2, l, d == 0));
 }
 
-// The flat list of work of text_tc.cu's kernel: for each sequence, K/V head and tile of N rows, the sequence's tiles
-// of 128 tokens (one entry for all of them where `whole`).  A block takes `share` neighbouring entries, so blocks are
-// even whatever the lengths are, and most units are one block's.
-struct Piece {
-  Span sp;
-  int seq, head, tile;
-  int first, tiles, of;   // the unit's token tiles from here on, how many it has
-};
-__device__ __forceinline__ long long entries_of(const AttnArgs& a, const Span& sp, int N, bool whole) {
-  const int rows = (sp.rows * (a.q_heads / a.c.heads) + N - 1) / N;
-  return sp.ok ? (long long)a.c.heads * rows * (whole ? 1 : (sp.len + 127) / 128) : 0;
-}
-// All entries (at < 0), or where entry `at` is (at less than all).  The whole warp calls it.
-__device__ __forceinline__ long long find_entry(const AttnArgs& a, int N, bool whole, long long at, Piece* p) {
-  const int lane = threadIdx.x & 31;
-  long long base = 0;
-  for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
-    const int s = s0 + lane;
-    Span sp = {};
-    if (s < a.b.n_seqs) sp = span_of(a.b, a.c.page_log2, s, a.max_len, a.max_rows);
-    long long sum = s < a.b.n_seqs ? entries_of(a, sp, N, whole) : 0;
-#pragma unroll
-    for (int x = 1; x < 32; x *= 2) {
-      const long long y = __shfl_up_sync(~0u, sum, x);
-      if (lane >= x) sum += y;
-    }
-    const uint32_t behind = __ballot_sync(~0u, at >= 0 && at < base + sum);
-    if (behind) {
-      const int l = __ffs(behind) - 1;
-      const long long before = l ? __shfl_sync(~0u, sum, max(l - 1, 0)) : 0;
-      p->seq = s0 + l;
-      p->sp.first = __shfl_sync(~0u, sp.first, l);
-      p->sp.rows = __shfl_sync(~0u, sp.rows, l);
-      p->sp.len = __shfl_sync(~0u, sp.len, l);
-      p->sp.ok = true;
-      const int rows = (p->sp.rows * (a.q_heads / a.c.heads) + N - 1) / N;
-      p->of = (p->sp.len + 127) / 128;
-      const int in = (int)(at - base - before), each = whole ? 1 : p->of, unit = in / each;
-      p->head = unit / rows;
-      p->tile = unit % rows;
-      p->first = whole ? 0 : in % each;
-      p->tiles = p->of - p->first;
-      return at;
-    }
-    base += __shfl_sync(~0u, sum, 31);
-  }
-  return base;
-}
-
 // The rows of a sequence whose numbers do not fit together see no text token.
 template <bool F32, int D>
 __device__ __forceinline__ void finish_misfit(const AttnArgs& a, const Span& sp, int seq, int head, int G) {
@@ -195,9 +136,6 @@ __device__ __forceinline__ void finish_misfit(const AttnArgs& a, const Span& sp,
       finish4<F32>(a, (long long)row * a.q_heads + head * G + i / (D / 4), i % (D / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f),
                    -INFINITY, 0.f);
 }
-
-// Sums the pieces of the units that blocks share (text_parts.cu).
-cudaError_t launch_flat_combine(const AttnArgs& a, const Flat& f, int blocks, cudaStream_t st);
 
 }  // namespace text
 }  // namespace tactkv

@@ -10,7 +10,7 @@ namespace text {
 #define TACTKV_DECL(D) cudaError_t launch_parts_##D(int, bool, const AttnArgs&, const Parts&, cudaStream_t);
 TACTKV_FOR_D(TACTKV_DECL)
 #undef TACTKV_DECL
-#define TACTKV_DECL(D) cudaError_t launch_tc_##D(int, const AttnArgs&, const Flat&, int, cudaStream_t);
+#define TACTKV_DECL(D) cudaError_t launch_tc_##D(int, const AttnArgs&, const Parts&, cudaStream_t);
 TACTKV_DECL(64) TACTKV_DECL(128) TACTKV_DECL(192) TACTKV_DECL(256)
 #undef TACTKV_DECL
 
@@ -18,15 +18,21 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// out, m and l of (row, query head) number `at`: the sums of n parts, each to the largest maximum, in the parts' order.
-// part(i): the place of part i.
-template <bool F32, class F>
-__device__ __forceinline__ void sum_parts(const AttnArgs& a, const float* o, const float2* ml, int n, long long at, F part) {
+// out, m and l of one (row, query head): its parts' sums, each to the largest maximum, in the parts' order.
+template <bool F32>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, const Parts p) {
   __shared__ float4 sum[kThreads];
   __shared__ float part_l[kThreads];
-  const int D = a.c.head_dim, cols = D / 4, groups = kThreads / cols, g = threadIdx.x / cols, d = threadIdx.x % cols * 4;
+  const int D = a.c.head_dim, G = a.q_heads / a.c.heads;
+  const int unit = blockIdx.y, tile = unit % p.tiles, head = unit / p.tiles % a.c.heads, seq = unit / p.tiles / a.c.heads;
+  const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
+  const int row = tile * p.tile_rows + blockIdx.x;
+  if (!sp.ok || row >= sp.rows * G) return;
+  const int n = max(1, (sp.len + p.tokens - 1) / p.tokens);
+  const long long stride = (long long)gridDim.y * p.tile_rows, at = (long long)unit * p.tile_rows + blockIdx.x;
+  const int cols = D / 4, groups = kThreads / cols, g = threadIdx.x / cols, d = threadIdx.x % cols * 4;
   float m = -INFINITY;
-  for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, ml[part(i)].x);
+  for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, p.ml[i * stride + at].x);
 #pragma unroll
   for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
   const float safe = m == -INFINITY ? 0.f : m;
@@ -35,11 +41,11 @@ __device__ __forceinline__ void sum_parts(const AttnArgs& a, const float* o, con
   if (g < groups) {
 #pragma unroll 4
     for (int i = g; i < n; i += groups) {
-      const float2 x = ml[part(i)];
-      const float4 y = *reinterpret_cast<const float4*>(o + part(i) * D + d);
-      const float f = exp2f(x.x - safe);
-      l += x.y * f;
-      v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
+      const float2 ml = p.ml[i * stride + at];
+      const float4 x = *reinterpret_cast<const float4*>(p.o + (i * stride + at) * D + d);
+      const float f = exp2f(ml.x - safe);
+      l += ml.y * f;
+      v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
     }
   }
   sum[threadIdx.x] = v;
@@ -51,48 +57,10 @@ __device__ __forceinline__ void sum_parts(const AttnArgs& a, const float* o, con
     l += part_l[i * cols + threadIdx.x];
     v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
   }
-  finish4<F32>(a, at, d, v, m, l);
-}
-
-template <bool F32>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, const Parts p) {
-  const int G = a.q_heads / a.c.heads;
-  const int unit = blockIdx.y, tile = unit % p.tiles, head = unit / p.tiles % a.c.heads, seq = unit / p.tiles / a.c.heads;
-  const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
-  const int row = tile * p.tile_rows + blockIdx.x;
-  if (!sp.ok || row >= sp.rows * G) return;
-  const int n = max(1, (sp.len + p.tokens - 1) / p.tokens);
-  const long long stride = (long long)gridDim.y * p.tile_rows, at = (long long)unit * p.tile_rows + blockIdx.x;
-  sum_parts<F32>(a, p.o, p.ml, n, (long long)(sp.first + row / G) * a.q_heads + head * G + row % G,
-                 [&](int i) { return i * stride + at; });
-}
-
-// Block (x, y): the unit across the border between blocks x and x + 1 of the list of work, if that is the unit's first
-// border; its row y.
-__global__ void __launch_bounds__(kThreads) flat_combine_kernel(const AttnArgs a, const Flat f) {
-  const int blocks = gridDim.x + 1, G = a.q_heads / a.c.heads;
-  Piece piece;
-  const long long entries = find_entry(a, f.rows, false, -1, &piece);
-  const long long share = max((entries + blocks - 1) / blocks, (long long)kLeastShare), border = (blockIdx.x + 1) * share;
-  if (border >= entries) return;
-  find_entry(a, f.rows, false, border, &piece);
-  const long long from = border - piece.first, to = from + piece.of;
-  if (piece.first == 0 || from < border - share) return;
-  const int row = piece.tile * f.rows + blockIdx.y;
-  if (row >= piece.sp.rows * G) return;
-  const int n = (int)((to - 1) / share) - blockIdx.x + 1;
-  // the unit is the first piece of every block but the one it begins in, unless it begins with that block
-  const long long begin = 2 * blockIdx.x + (from > border - share);
-  sum_parts<false>(a, f.o, f.ml, n, (long long)(piece.sp.first + row / G) * a.q_heads + piece.head * G + row % G,
-                   [&](int i) { return (i ? 2ll * (blockIdx.x + i) : begin) * f.rows + blockIdx.y; });
+  finish4<F32>(a, (long long)(sp.first + row / G) * a.q_heads + head * G + row % G, d, v, m, l);
 }
 
 }  // namespace
-
-cudaError_t launch_flat_combine(const AttnArgs& a, const Flat& f, int blocks, cudaStream_t st) {
-  flat_combine_kernel<<<dim3(blocks - 1, f.rows), kThreads, 0, st>>>(a, f);
-  return cudaGetLastError();
-}
 
 size_t attention_workspace(int head_dim) {
   return (size_t)kMaxParts * kPartRows(head_dim) * (head_dim * sizeof(float) + sizeof(float2));
@@ -100,32 +68,29 @@ size_t attention_workspace(int head_dim) {
 
 cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspace, cudaStream_t st) {
   const int D = a.c.head_dim, rows = a.max_rows * (a.q_heads / a.c.heads);
-  float* o = static_cast<float*>(workspace);
-  float2* ml = reinterpret_cast<float2*>(o + (size_t)kMaxParts * kPartRows(D) * D);
-  cudaError_t e = cudaErrorInvalidValue;
-  if (!f32 && D % 64 == 0 && !getenv("NOTC")) {
-    const Flat f = {0, false, o, ml};
-    switch (D) {
-#define TACTKV_CASE(D) case D: e = launch_tc_##D(fmt, a, f, rows, st); break;
-      TACTKV_CASE(64) TACTKV_CASE(128) TACTKV_CASE(192) TACTKV_CASE(256)
-#undef TACTKV_CASE
-    }
-    return e;
-  }
+  const bool tc = !f32 && D % 64 == 0 && !getenv("NOTC");
   Parts p;
-  p.tile_rows = rows <= 8 ? 8 : (rows <= 16 || D > kWideDim ? 16 : 32);
+  if (tc) p.tile_rows = rows <= 16 ? 16 : (rows <= 32 || D > kWideDim ? 32 : 64);
+  else p.tile_rows = rows <= 8 ? 8 : (rows <= 16 || D > kWideDim ? 16 : 32);
   p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   const long long units = (long long)a.b.n_seqs * a.c.heads * p.tiles;
-  const long long most = (a.max_len + kLeastPart - 1) / kLeastPart;
-  p.count = (int)std::max(1ll, std::min(most, kMaxParts / units));
-  p.tokens = std::max(kLeastPart, ((a.max_len + p.count - 1) / p.count + 63) / 64 * 64);
+  const int grain = 128;
+  int least = kLeastPart; if (getenv("LEAST")) least = atoi(getenv("LEAST"));
+  int mp = tc ? 148 : kMaxParts; if (getenv("MP")) mp = atoi(getenv("MP"));
+  const long long most = (a.max_len + least - 1) / least;
+  p.count = (int)std::max(1ll, std::min(most, mp / units));
+  p.tokens = std::max(least, ((a.max_len + p.count - 1) / p.count + grain - 1) / grain * grain);
   p.count = std::max(1, (a.max_len + p.tokens - 1) / p.tokens);
-  p.o = o;
-  p.ml = ml;
+  p.o = static_cast<float*>(workspace);
+  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kMaxParts * kPartRows(D) * D);
+  cudaError_t e = cudaErrorInvalidValue;
   switch (D) {
 #define TACTKV_CASE(D) case D: e = launch_parts_##D(fmt, f32, a, p, st); break;
-    TACTKV_FOR_D(TACTKV_CASE)
+#define TACTKV_CASE_TC(D) case D: e = tc ? launch_tc_##D(fmt, a, p, st) : launch_parts_##D(fmt, f32, a, p, st); break;
+    TACTKV_CASE(32) TACTKV_CASE_TC(64) TACTKV_CASE(96) TACTKV_CASE_TC(128) TACTKV_CASE(160) TACTKV_CASE_TC(192)
+    TACTKV_CASE(224) TACTKV_CASE_TC(256)
 #undef TACTKV_CASE
+#undef TACTKV_CASE_TC
   }
   if (e != cudaSuccess || p.count == 1) return e;
   const dim3 grid(p.tile_rows, (unsigned)units);

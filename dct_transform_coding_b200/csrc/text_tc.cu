@@ -74,11 +74,6 @@ struct Shape {
   static_assert(N * (D + 4) * 4 <= kOps + (kCoded ? 0 : kSlots * kSlot), "the sums take the operands' place");
 };
 
-struct Job {            // a piece: part or all of a unit's tokens
-  long long next, end, after;                     // entries of the list: where this piece begins, the share's end, where the next begins
-  int number, seq, head, tile, first, tiles, of, row, rows, len;
-};
-
 struct Bars {
   uint64_t slot_full[kMaxSlots], slot_free[kMaxSlots], op_full[3], op_free[3], tops_full[4],
       s_full[2], p_full[2], pv_done[2], drain;
@@ -159,7 +154,7 @@ __device__ __forceinline__ float reduce_rows(float (&v)[R]) {
 
 template <int FMT, int N>
 __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
-    tc_kernel(const AttnArgs a, const Flat flat, const __grid_constant__ CUtensorMap k_map,
+    tc_kernel(const AttnArgs a, const Parts parts, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<FMT, N>;
   constexpr bool kCoded = Sh::kCoded;
@@ -186,44 +181,21 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = a.q_heads / a.c.heads;
-  constexpr int kProducer = 4 * Sh::kWGs, kIssuer = kProducer + 1;
-  for (int seq = blockIdx.x; seq < a.b.n_seqs; seq += gridDim.x) {
-    const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
-    if (!sp.ok)
-      for (int head = 0; head < a.c.heads; ++head) finish_misfit<false, D>(a, sp, seq, head, G);
+  const int part = blockIdx.x, seq = blockIdx.z, tiles = gridDim.y / a.c.heads;
+  const int head = blockIdx.y / tiles, tile = blockIdx.y % tiles;
+  const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
+  if (!sp.ok) {                                   // the sequence's rows see no text token
+    if (part == 0 && tile == 0) finish_misfit<false, D>(a, sp, seq, head, G);
+    return;
   }
-  // The block's share of the list.  Its pieces are found by one warp and passed on in shared memory.
-  volatile Job* job = reinterpret_cast<Job*>(misc + 640);
-  if (warp == 0) {
-    const long long entries = find_entry(a, N, flat.whole, -1, nullptr);
-    const long long share = max((entries + gridDim.x - 1) / gridDim.x, (long long)(flat.whole ? 1 : kLeastShare));
-    if (lane == 0) job->next = blockIdx.x * share, job->end = min(entries, (blockIdx.x + 1) * share), job->number = -1;
-  }
-  if (warp == kIssuer) tc::tmem_alloc(tmem_slot, Sh::kTmem);
-  __syncthreads();
-  while (job->next < job->end) {
-  if (warp == 0) {
-    Piece p;
-    const long long next = job->next;
-    find_entry(a, N, flat.whole, next, &p);
-    __syncwarp();
-    if (lane == 0) {
-      const int n = flat.whole ? p.of : (int)min((long long)p.tiles, job->end - next);
-      job->seq = p.seq, job->head = p.head, job->tile = p.tile, job->first = p.first, job->tiles = n, job->of = p.of;
-      job->row = p.sp.first, job->rows = p.sp.rows, job->len = p.sp.len, job->number = job->number + 1;
-      job->after = next + (flat.whole ? 1 : n);
-    }
-  }
-  __syncthreads();
-  const bool first_piece = job->number == 0;
-  const Span sp = {job->row, job->rows, job->len, true};
-  const int seq = job->seq, head = job->head;
-  const int M = sp.rows * G, row0 = job->tile * N, before = sp.len - sp.rows;
-  const int t0 = job->first * TT, n_tiles = job->tiles;
+  const int M = sp.rows * G, row0 = tile * N, before = sp.len - sp.rows;
+  const int t0 = part * parts.tokens;
+  if (row0 >= M || t0 >= sp.len) return;
+  const int n_tiles = (min(sp.len - t0, parts.tokens) + TT - 1) / TT;
 
-  // K's tiles are copied one ahead of V's: K0 K1 V0 K2 V1 .. V(n-1).  bfloat16 slots follow one another in that
-  // order.  Raw slots are rings of their own for K and V and for each half: a group of decoders sees every phase of its
-  // slots' barriers, and so can tell them apart.
+  // bfloat16: K's tiles are copied one ahead of V's, K0 K1 V0 K2 V1 .. V(n-1), and slots follow one another in that
+  // order.  Coded: raw slots are rings of their own for K and V and for each half (a group of decoders sees every phase
+  // of its slots' barriers, and so can tell them apart), and copies go K0 V0 K1 V1 ..
   constexpr int kRing = kCoded ? Sh::kSlots / 4 : Sh::kSlots;
   auto turn_of = [&](int i, int kv) { return kCoded ? i : (!kv ? max(2 * i - 1, 0) : (i < n_tiles - 1 ? 2 * i + 2 : 2 * n_tiles - 1)); };
   auto slot_of = [&](int i, int kv, int half) { return (kCoded ? (kv * 2 + half) * kRing : 0) + turn_of(i, kv) % kRing; };
@@ -275,11 +247,10 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       };
 
   // ---- set up: barriers and the first copy, tensor memory, the queries' operand ----
+  constexpr int kProducer = 4 * Sh::kWGs, kIssuer = kProducer + 1;
   if (warp == kProducer) {
     if (lane == 0) {
-      if (!first_piece)
-        for (int i = 0; i < (int)(sizeof(Bars) / 8); ++i) tc::mbar_inval(reinterpret_cast<uint64_t*>(bars) + i);
-      for (int i = 0; i < kMaxSlots; ++i) {
+      for (int i = 0; i < Sh::kSlots; ++i) {
         tc::mbar_init(&bars->slot_full[i], 1);
         tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders / 4 : 1);
       }
@@ -295,14 +266,20 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       tc::mbar_init(&bars->pv_done[1], 1);
       tc::mbar_init(&bars->drain, 1);
       tc::fence_mbar_init();
-      if (first_piece) *dead = 0;
+      *dead = 0;
       odd_nodes[0] = odd_nodes[1] = 0;
       *odd_tile = 0;
     }
     __syncwarp();
     find(0);
     copy(0, 0);
-  } else if (warp != kIssuer) {
+    if constexpr (kCoded) {
+      at = at_next, good = good_next;
+      copy(1, 0);
+    }
+  } else if (warp == kIssuer) {
+    tc::tmem_alloc(tmem_slot, Sh::kTmem);
+  } else {
     constexpr int E = D / 32, kStagers = Sh::kThreads / 32 - 2, kMine = (N + kStagers - 1) / kStagers;
     const int stager = warp < kProducer ? warp : warp - 2;
     uint32_t w[kMine][E / 2];                      // a warp per row, lane i with its elements i * E ..; all rows' loads first
@@ -359,12 +336,13 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   if (warp == kProducer) {
     // ------------------------------------------------------------------------------ producer ---
     for (int i = 0; i < n_tiles && copies_ok; ++i) {
-      at = at_next, good = good_next;
-      if (i + 1 < n_tiles) {
+      if (i || !kCoded) at = at_next, good = good_next;
+      if (kCoded && i) copy(1, i);
+      if (copies_ok && i + 1 < n_tiles) {
         find(i + 1);
         copy(0, i + 1);
       }
-      if (copies_ok) copy(1, i);
+      if (!kCoded && copies_ok) copy(1, i);
     }
     // Copies in flight when a wait expired land before the block ends.
     if (!copies_ok)
@@ -420,13 +398,9 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         tc::mma_commit(&bars->pv_done[i & 1]);
         release(i, 1);
       }
-      // Every product and every arrival is in before the barriers and tensor memory are used anew.
-      tc::mma_commit(&bars->drain);
-      wait(&bars->drain, 0, nullptr);
-      for (int kv = 0; kv < 2 && ok; ++kv) {
-        const int i = n_tiles - 1;
-        if (kCoded) wait(&bars->op_free[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, nullptr);
-        else wait(&bars->slot_free[slot_of(i, kv, 0)], round_of(i, kv) & 1, nullptr);
+      if (!ok) {                                   // products in flight end before tensor memory is released
+        tc::mma_commit(&bars->drain);
+        wait(&bars->drain, 0, nullptr);
       }
     }
     __syncwarp();
@@ -667,22 +641,21 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (row < M) {
         const float2 ml = row_ml[n];
         const float* from = sums + n * (D + 4) + tid % 8 * 4;
-        if (n_tiles == job->of) {
+        if (parts.count == 1) {
           const long long at = (long long)(sp.first + row / G) * a.q_heads + head * G + row % G;
           const RowEnd e = end_row(a, at, ml.x, ml.y, tid % 8 == 0);
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
             finish4<false>(a, at, tid % 8 * 4 + 32 * k, *reinterpret_cast<const float4*>(from + 32 * k), e);
         } else {
-          const long long to = (2ll * blockIdx.x + !first_piece) * N + n;
+          const long long to = ((long long)part * gridDim.z * gridDim.y + seq * gridDim.y + blockIdx.y) * N + n;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            *reinterpret_cast<float4*>(flat.o + to * D + tid % 8 * 4 + 32 * k) = *reinterpret_cast<const float4*>(from + 32 * k);
-          if (tid % 8 == 0) flat.ml[to] = ml;
+            *reinterpret_cast<float4*>(parts.o + to * D + tid % 8 * 4 + 32 * k) = *reinterpret_cast<const float4*>(from + 32 * k);
+          if (tid % 8 == 0) parts.ml[to] = ml;
         }
       }
     }
-    tc::fence_proxy_async();                       // the next piece's copies come after these stores
     tc::fence_before_sync();
   } else if constexpr (kCoded) {
     // ------------------------------------------------------------------------------ decoders ---
@@ -819,11 +792,10 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     }
   }
   __syncthreads();
-  tc::fence_after_sync();
-  if (threadIdx.x == 0) job->next = *dead ? job->end : job->after;
-  __syncthreads();
+  if (warp == kIssuer) {
+    tc::fence_after_sync();
+    tc::tmem_free(tmem, Sh::kTmem);
   }
-  if (warp == kIssuer) tc::tmem_free(*tmem_slot, Sh::kTmem);
 }
 
 bool make_map(const AttnArgs& a, int kv, CUtensorMap* map) {
@@ -846,7 +818,7 @@ bool make_map(const AttnArgs& a, int kv, CUtensorMap* map) {
 }
 
 template <int FMT, int N>
-cudaError_t launch(const AttnArgs& a, Flat f, int rows, cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
   using Sh = Shape<FMT, N>;
   // the kernel's shared memory is set once for each device (twice by two threads at once does no harm)
   static std::atomic<unsigned long long> set{0};
@@ -860,20 +832,14 @@ cudaError_t launch(const AttnArgs& a, Flat f, int rows, cudaStream_t st) {
   }
   CUtensorMap maps[2] = {};
   if (FMT == kBf16 && !(make_map(a, 0, &maps[0]) && make_map(a, 1, &maps[1]))) return cudaErrorInvalidValue;
-  f.rows = N;
-  const long long units = (long long)a.b.n_seqs * a.c.heads * ((rows + N - 1) / N), tiles = (a.max_len + TT - 1) / TT;
-  f.whole = tiles <= kLeastShare;
-  const long long most = f.whole ? units : std::max(units * tiles / kLeastShare, 1ll);
-  const int blocks = (int)std::min(most, (long long)kSms * Sh::kCtas);
-  tc_kernel<FMT, N><<<blocks, Sh::kThreads, Sh::kSmem, st>>>(a, f, maps[0], maps[1]);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess || f.whole || blocks == 1 ? e : launch_flat_combine(a, f, blocks, st);
+  tc_kernel<FMT, N><<<dim3(p.count, a.c.heads * p.tiles, a.b.n_seqs), Sh::kThreads, Sh::kSmem, st>>>(a, p, maps[0], maps[1]);
+  return cudaGetLastError();
 }
 template <int FMT>
-cudaError_t launch(const AttnArgs& a, const Flat& f, int rows, cudaStream_t st) {
-  if (rows <= 16) return launch<FMT, 16>(a, f, rows, st);
-  if (rows <= 32 || D > kWideDim) return launch<FMT, 32>(a, f, rows, st);
-  if constexpr (D <= kWideDim) return launch<FMT, 64>(a, f, rows, st);
+cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
+  if (p.tile_rows == 16) return launch<FMT, 16>(a, p, st);
+  if (p.tile_rows == 32) return launch<FMT, 32>(a, p, st);
+  if constexpr (D <= kWideDim) return launch<FMT, 64>(a, p, st);
   return cudaErrorInvalidValue;
 }
 
@@ -881,8 +847,8 @@ cudaError_t launch(const AttnArgs& a, const Flat& f, int rows, cudaStream_t st) 
 
 #define TACTKV_CAT_(x, y) x##y
 #define TACTKV_CAT(x, y) TACTKV_CAT_(x, y)
-cudaError_t TACTKV_CAT(launch_tc_, TACTKV_TEXT_D)(int fmt, const AttnArgs& a, const Flat& f, int rows, cudaStream_t st) {
-  return fmt == kBf16 ? launch<kBf16>(a, f, rows, st) : (fmt == kFp8 ? launch<kFp8>(a, f, rows, st) : launch<kFp4>(a, f, rows, st));
+cudaError_t TACTKV_CAT(launch_tc_, TACTKV_TEXT_D)(int fmt, const AttnArgs& a, const Parts& p, cudaStream_t st) {
+  return fmt == kBf16 ? launch<kBf16>(a, p, st) : (fmt == kFp8 ? launch<kFp8>(a, p, st) : launch<kFp4>(a, p, st));
 }
 
 }  // namespace text
