@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
 
   // bfloat16: K's tiles are copied one ahead of V's, K0 K1 V0 K2 V1 .. V(n-1), and slots follow one another in that
   // order.  Coded: raw slots are rings of their own for K and V and for each half (a group of decoders sees every phase
-  // of its slots' barriers, and so can tell them apart), and copies go K0 V0 K1 V1 ..
+  // of its slots' barriers, and so can tell them apart), and V0 comes before K1.
   constexpr int kRing = kCoded ? Sh::kSlots / 4 : Sh::kSlots;
   auto turn_of = [&](int i, int kv) { return kCoded ? i : (!kv ? max(2 * i - 1, 0) : (i < n_tiles - 1 ? 2 * i + 2 : 2 * n_tiles - 1)); };
   auto slot_of = [&](int i, int kv, int half) { return (kCoded ? (kv * 2 + half) * kRing : 0) + turn_of(i, kv) % kRing; };
@@ -336,13 +336,12 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   if (warp == kProducer) {
     // ------------------------------------------------------------------------------ producer ---
     for (int i = 0; i < n_tiles && copies_ok; ++i) {
-      if (i || !kCoded) at = at_next, good = good_next;
-      if (kCoded && i) copy(1, i);
-      if (copies_ok && i + 1 < n_tiles) {
+      at = at_next, good = good_next;
+      if (i + 1 < n_tiles) {
         find(i + 1);
         copy(0, i + 1);
       }
-      if (!kCoded && copies_ok) copy(1, i);
+      if (copies_ok && !(kCoded && i == 0)) copy(1, i);
     }
     // Copies in flight when a wait expired land before the block ends.
     if (!copies_ok)
