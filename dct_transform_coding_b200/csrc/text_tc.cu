@@ -249,29 +249,29 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   // ---- set up: barriers and the first copy, tensor memory, the queries' operand ----
   constexpr int kProducer = 4 * Sh::kWGs, kIssuer = kProducer + 1;
   if (warp == kProducer) {
+    find(0);
+    if (lane < Sh::kSlots) {
+      tc::mbar_init(&bars->slot_full[lane], 1);
+      tc::mbar_init(&bars->slot_free[lane], kCoded ? Sh::kDecoders / 4 : 1);
+    }
+    if (lane < 4) tc::mbar_init(&bars->tops_full[lane], 2);
+    if (lane < 3) {                                // K's operand, V's (one or two)
+      tc::mbar_init(&bars->op_full[lane], kCoded ? Sh::kDecoders / 2 : 1);
+      tc::mbar_init(&bars->op_free[lane], 1);
+    }
+    if (lane < 2) {
+      tc::mbar_init(&bars->s_full[lane], 1);
+      tc::mbar_init(&bars->p_full[lane], 128 * Sh::kWGs);
+      tc::mbar_init(&bars->pv_done[lane], 1);
+      odd_nodes[lane] = 0;
+    }
     if (lane == 0) {
-      for (int i = 0; i < Sh::kSlots; ++i) {
-        tc::mbar_init(&bars->slot_full[i], 1);
-        tc::mbar_init(&bars->slot_free[i], kCoded ? Sh::kDecoders / 4 : 1);
-      }
-      for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->tops_full[i], 2);
-      for (int i = 0; i < 3; ++i) {                // K's operand, V's (one or two)
-        tc::mbar_init(&bars->op_full[i], kCoded ? Sh::kDecoders / 2 : 1);
-        tc::mbar_init(&bars->op_free[i], 1);
-      }
-      for (int i = 0; i < 2; ++i) tc::mbar_init(&bars->s_full[i], 1);
-      tc::mbar_init(&bars->p_full[0], 128 * Sh::kWGs);
-      tc::mbar_init(&bars->p_full[1], 128 * Sh::kWGs);
-      tc::mbar_init(&bars->pv_done[0], 1);
-      tc::mbar_init(&bars->pv_done[1], 1);
       tc::mbar_init(&bars->drain, 1);
-      tc::fence_mbar_init();
       *dead = 0;
-      odd_nodes[0] = odd_nodes[1] = 0;
       *odd_tile = 0;
     }
+    tc::fence_mbar_init();
     __syncwarp();
-    find(0);
     copy(0, 0);
     if constexpr (kCoded) {
       at = at_next, good = good_next;
@@ -436,9 +436,11 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         x[n] = fmaf(x[n], k_scale * f.x, f.y), x[n + 1] = fmaf(x[n + 1], k_scale * f.z, f.w);
       }
       if (tail || bad) {
+        const uint32_t* half = reinterpret_cast<const uint32_t*>(words + rows0) + (node >> 5 & 1);
+        const uint32_t bit = node >= 0 && !absent ? 1u << (node & 31) : 0u;   // 0: every row sees the token, or none
+        const uint32_t none = absent ? 0u : ~0u;
 #pragma unroll
-        for (int n = 0; n < R; ++n)
-          if (absent || (node >= 0 && !(words[rows0 + n] >> node & 1))) x[n] = -INFINITY;
+        for (int n = 0; n < R; ++n) x[n] = (half[2 * n] & bit) == bit && none ? x[n] : -INFINITY;
       }
       float most = -INFINITY;
 #pragma unroll
