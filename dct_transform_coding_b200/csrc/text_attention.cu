@@ -514,6 +514,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     }
   }
   copy_wait<0>();
+  let_next_start();
 
   // ---- the warps' sums, to the rows' true maxima ----
   __syncthreads();                                 // the ring is done: its place takes the sums

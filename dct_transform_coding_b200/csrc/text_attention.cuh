@@ -19,11 +19,16 @@ constexpr int kWideDim = 128;      // up to this head_dim a unit may have 32 row
 
 constexpr int kPartRows(int D) { return D <= kWideDim ? 64 : 32; }
 
+constexpr int kSms = 148;
+// Up to one tile of text_tc.cu's the kernel of text_attention.cu is used: its start is shorter (128 tokens, 4 heads x 128,
+// 8 bits: 7.0 against 9.1 us; from 256 tokens on the other is, 9.6 against 10.1, 4096: 79 against 63).
+constexpr int kOneTile = 128;
+
 // A unit is (sequence, K/V head, tile of tile_rows rows), numbered in that order.
 struct Parts {
-  int tile_rows;       // 8, 16 or 32
+  int tile_rows;       // 8, 16, 32 or 64
   int tiles;           // for max_rows * G rows
-  int tokens;          // per part, a multiple of 64
+  int tokens;          // per part, a multiple of 128
   int count;           // parts of the longest sequence
   float* o;            // [count][unit][tile_rows][D] sums of exp2(z - m) V
   float2* ml;          // [count][unit][tile_rows] m (log2), l
@@ -135,6 +140,20 @@ __device__ __forceinline__ void finish_misfit(const AttnArgs& a, const Span& sp,
     for (int i = threadIdx.x; i < G * (D / 4); i += blockDim.x)
       finish4<F32>(a, (long long)row * a.q_heads + head * G + i / (D / 4), i % (D / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f),
                    -INFINITY, 0.f);
+}
+
+// The combining kernel may start, and wait for this one, while this block ends.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+// The split of a launch into at most `blocks` blocks, and each sequence into parts of at least `least` tokens.
+inline void plan(const AttnArgs& a, int tile_rows, int blocks, int least, Parts& p) {
+  p.tile_rows = tile_rows;
+  p.tiles = (a.max_rows * (a.q_heads / a.c.heads) + tile_rows - 1) / tile_rows;
+  const long long units = (long long)a.b.n_seqs * a.c.heads * p.tiles, most = (a.max_len + least - 1) / least;
+  p.count = (int)std::max(1ll, std::min(most, blocks / units));
+  p.tokens = std::max(least, ((a.max_len + p.count - 1) / p.count + 127) / 128 * 128);
+  p.count = std::max(1, (a.max_len + p.tokens - 1) / p.tokens);
 }
 
 }  // namespace text

@@ -1,6 +1,4 @@
 // Attention over the text cache: the launch plan, and the sum over a sequence's parts.
-#include <cstdlib>
-
 #include "text_attention.cuh"
 
 namespace tactkv {
@@ -10,7 +8,7 @@ namespace text {
 #define TACTKV_DECL(D) cudaError_t launch_parts_##D(int, bool, const AttnArgs&, const Parts&, cudaStream_t);
 TACTKV_FOR_D(TACTKV_DECL)
 #undef TACTKV_DECL
-#define TACTKV_DECL(D) cudaError_t launch_tc_##D(int, const AttnArgs&, const Parts&, cudaStream_t);
+#define TACTKV_DECL(D) cudaError_t launch_tc_##D(int, const AttnArgs&, Parts&, cudaStream_t);
 TACTKV_DECL(64) TACTKV_DECL(128) TACTKV_DECL(192) TACTKV_DECL(256)
 #undef TACTKV_DECL
 
@@ -23,6 +21,7 @@ template <bool F32>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, const Parts p) {
   __shared__ float4 sum[kThreads];
   __shared__ float part_l[kThreads];
+  wait_for_previous();
   const int D = a.c.head_dim, G = a.q_heads / a.c.heads;
   const int unit = blockIdx.y, tile = unit % p.tiles, head = unit / p.tiles % a.c.heads, seq = unit / p.tiles / a.c.heads;
   const Span sp = span_of(a.b, a.c.page_log2, seq, a.max_len, a.max_rows);
@@ -68,35 +67,35 @@ size_t attention_workspace(int head_dim) {
 
 cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspace, cudaStream_t st) {
   const int D = a.c.head_dim, rows = a.max_rows * (a.q_heads / a.c.heads);
-  const bool tc = !f32 && D % 64 == 0 && !getenv("NOTC");
   Parts p;
-  if (tc) p.tile_rows = rows <= 16 ? 16 : (rows <= 32 || D > kWideDim ? 32 : 64);
-  else p.tile_rows = rows <= 8 ? 8 : (rows <= 16 || D > kWideDim ? 16 : 32);
-  p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  const long long units = (long long)a.b.n_seqs * a.c.heads * p.tiles;
-  const int grain = 128;
-  int least = kLeastPart; if (getenv("LEAST")) least = atoi(getenv("LEAST"));
-  int mp = tc ? 148 : kMaxParts; if (getenv("MP")) mp = atoi(getenv("MP"));
-  const long long most = (a.max_len + least - 1) / least;
-  p.count = (int)std::max(1ll, std::min(most, mp / units));
-  p.tokens = std::max(least, ((a.max_len + p.count - 1) / p.count + grain - 1) / grain * grain);
-  p.count = std::max(1, (a.max_len + p.tokens - 1) / p.tokens);
   p.o = static_cast<float*>(workspace);
   p.ml = reinterpret_cast<float2*>(p.o + (size_t)kMaxParts * kPartRows(D) * D);
   cudaError_t e = cudaErrorInvalidValue;
-  switch (D) {
-#define TACTKV_CASE(D) case D: e = launch_parts_##D(fmt, f32, a, p, st); break;
-#define TACTKV_CASE_TC(D) case D: e = tc ? launch_tc_##D(fmt, a, p, st) : launch_parts_##D(fmt, f32, a, p, st); break;
-    TACTKV_CASE(32) TACTKV_CASE_TC(64) TACTKV_CASE(96) TACTKV_CASE_TC(128) TACTKV_CASE(160) TACTKV_CASE_TC(192)
-    TACTKV_CASE(224) TACTKV_CASE_TC(256)
+  if (!f32 && D % 64 == 0 && a.max_len > kOneTile) {
+    switch (D) {
+#define TACTKV_CASE(D) case D: e = launch_tc_##D(fmt, a, p, st); break;
+      TACTKV_CASE(64) TACTKV_CASE(128) TACTKV_CASE(192) TACTKV_CASE(256)
 #undef TACTKV_CASE
-#undef TACTKV_CASE_TC
+    }
+  } else {
+    plan(a, rows <= 8 ? 8 : (rows <= 16 || D > kWideDim ? 16 : 32), kMaxParts, kLeastPart, p);
+    switch (D) {
+#define TACTKV_CASE(D) case D: e = launch_parts_##D(fmt, f32, a, p, st); break;
+      TACTKV_FOR_D(TACTKV_CASE)
+#undef TACTKV_CASE
+    }
   }
   if (e != cudaSuccess || p.count == 1) return e;
-  const dim3 grid(p.tile_rows, (unsigned)units);
-  if (f32) combine_kernel<true><<<grid, kThreads, 0, st>>>(a, p);
-  else combine_kernel<false><<<grid, kThreads, 0, st>>>(a, p);
-  return cudaGetLastError();
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.tile_rows, a.b.n_seqs * a.c.heads * p.tiles);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return f32 ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a, p) : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a, p);
 }
 
 }  // namespace text

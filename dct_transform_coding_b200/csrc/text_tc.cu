@@ -571,6 +571,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       tc::fence_before_sync();
       tc::mbar_arrive(&bars->p_full[i & 1]);
     }
+    let_next_start();
     if (ok) ok = wait(&bars->pv_done[(n_tiles - 1) & 1], (n_tiles - 1) / 2 & 1, dead);
     if (bar_or(5, 128 * Sh::kWGs, !ok || *dead)) {
       if (tid == 0) atomicCAS(a.status, 0u, (unsigned int)TACTKV_TIMEOUT);
@@ -819,7 +820,7 @@ bool make_map(const AttnArgs& a, int kv, CUtensorMap* map) {
 }
 
 template <int FMT, int N>
-cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
   using Sh = Shape<FMT, N>;
   // the kernel's shared memory is set once for each device (twice by two threads at once does no harm)
   static std::atomic<unsigned long long> set{0};
@@ -833,13 +834,15 @@ cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
   }
   CUtensorMap maps[2] = {};
   if (FMT == kBf16 && !(make_map(a, 0, &maps[0]) && make_map(a, 1, &maps[1]))) return cudaErrorInvalidValue;
+  plan(a, N, kSms * Sh::kCtas, 2 * TT, p);
   tc_kernel<FMT, N><<<dim3(p.count, a.c.heads * p.tiles, a.b.n_seqs), Sh::kThreads, Sh::kSmem, st>>>(a, p, maps[0], maps[1]);
   return cudaGetLastError();
 }
 template <int FMT>
-cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
-  if (p.tile_rows == 16) return launch<FMT, 16>(a, p, st);
-  if (p.tile_rows == 32) return launch<FMT, 32>(a, p, st);
+cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
+  const int rows = a.max_rows * (a.q_heads / a.c.heads);
+  if (rows <= 16) return launch<FMT, 16>(a, p, st);
+  if (rows <= 32 || D > kWideDim) return launch<FMT, 32>(a, p, st);
   if constexpr (D <= kWideDim) return launch<FMT, 64>(a, p, st);
   return cudaErrorInvalidValue;
 }
@@ -848,7 +851,7 @@ cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
 
 #define TACTKV_CAT_(x, y) x##y
 #define TACTKV_CAT(x, y) TACTKV_CAT_(x, y)
-cudaError_t TACTKV_CAT(launch_tc_, TACTKV_TEXT_D)(int fmt, const AttnArgs& a, const Parts& p, cudaStream_t st) {
+cudaError_t TACTKV_CAT(launch_tc_, TACTKV_TEXT_D)(int fmt, const AttnArgs& a, Parts& p, cudaStream_t st) {
   return fmt == kBf16 ? launch<kBf16>(a, p, st) : (fmt == kFp8 ? launch<kFp8>(a, p, st) : launch<kFp4>(a, p, st));
 }
 
