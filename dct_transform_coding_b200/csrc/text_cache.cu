@@ -18,36 +18,44 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kItem = 256;   // values of K and of V per warp
 
-// Eight neighbouring values from p: 16-byte loads, or two at a time where the alignment allows no more.
+// Eight neighbouring values from p, as they lie there: 16-byte loads, or two values at a time where the alignment allows
+// no more.
 template <bool F32, bool VEC>
-__device__ __forceinline__ void load8(const void* p, long long at, float (&x)[8]) {
-  if constexpr (F32) {
-    const float* q = static_cast<const float*>(p) + at;
+__device__ __forceinline__ void load8(const void* p, long long at, uint32_t (&w)[F32 ? 8 : 4]) {
+  constexpr int kWords = F32 ? 8 : 4, kBytes = F32 ? 4 : 2;
+  const unsigned char* q = static_cast<const unsigned char*>(p) + at * kBytes;
 #pragma unroll
-    for (int i = 0; i < 8; i += VEC ? 4 : 2) {
-      if constexpr (VEC) {
-        const float4 v = *reinterpret_cast<const float4*>(q + i);
-        x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(q + i);
-        x[i] = v.x, x[i + 1] = v.y;
-      }
-    }
-  } else {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + at;
-    uint32_t w[4];
+  for (int i = 0; i < kWords; i += VEC ? 4 : (F32 ? 2 : 1)) {
     if constexpr (VEC) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      const uint4 v = *reinterpret_cast<const uint4*>(q + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    } else if constexpr (F32) {
+      const uint2 v = *reinterpret_cast<const uint2*>(q + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y;
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(q + 2 * i);
+      w[i] = *reinterpret_cast<const uint32_t*>(q + 4 * i);
     }
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void values8(const uint32_t (&w)[F32 ? 8 : 4], float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = unpack_bf16x2(w[i]);
-      x[2 * i] = v.x, x[2 * i + 1] = v.y;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = F32 ? make_float2(__uint_as_float(w[F32 ? 2 * i : 0]), __uint_as_float(w[F32 ? 2 * i + 1 : 0])) : unpack_bf16x2(w[i]);
+    x[2 * i] = v.x, x[2 * i + 1] = v.y;
+  }
+}
+// The bits of the largest magnitude of eight values (above all numbers' for an infinity or NaN), as float32's.
+template <bool F32>
+__device__ __forceinline__ uint32_t amax8(const uint32_t (&w)[F32 ? 8 : 4]) {
+  if constexpr (F32) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    return m;
+  } else {
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    return max(m << 16, m & 0xFFFF0000u);
   }
 }
 template <bool F32, bool VEC>
@@ -111,94 +119,115 @@ __device__ __forceinline__ long long place_of(const Cache& c, const Batch& b, in
   return at;
 }
 
-template <int FMT, bool F32, bool VEC>
+// e / head_dim for e < 65536, inverse = ceil(2^32 / head_dim): the product is too large by less than e * 256 / 2^32.
+__device__ __forceinline__ int head_of(int e, uint32_t inverse) { return (int)__umulhi((uint32_t)e, inverse); }
+
+// PER items of a row to a warp: 1 where rows are few and every warp counts, more where there are enough, so that a
+// row is looked up once for them and their loads are under way together.
+template <int FMT, bool F32, bool VEC, int PER>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Cache c, const Batch b, const void* k, const void* v,
                                                           long long token_stride, long long head_stride,
                                                           void* k_values, void* v_values, unsigned int* status,
-                                                          int items) {
-  const long long item = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  const int row = (int)(item / items);
+                                                          int items, uint32_t inverse) {
+  const long long unit = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int row = (int)(unit / items);           // items: of a row, PER at a time
   if (row >= b.n_rows) return;
-  const int e = (int)(item % items) * kItem + (threadIdx.x & 31) * 8;
+  const int e0 = (int)(unit % items) * (PER * kItem) + (threadIdx.x & 31) * 8;
   const int width = c.heads * c.head_dim;
-  const bool mine = e < width;                 // whole groups of four lanes: width is a multiple of 32
-  const int head = mine ? e / c.head_dim : 0, d = mine ? e % c.head_dim : 0;
+  uint32_t in[PER][2][F32 ? 8 : 4];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = e0 + i * kItem;                // whole groups of four lanes are within the row: width is a multiple of 32
+    if (e < width) {
+      const int head = head_of(e, inverse);
+      const long long from = row * token_stride + head * head_stride + (e - head * c.head_dim);
+      load8<F32, VEC>(k, from, in[i][0]);
+      load8<F32, VEC>(v, from, in[i][1]);
+    }
+  }
   bool owned;
   const long long first = place_of(c, b, row, status, &owned);
   if (!owned || first < 0) return;
-  const long long from = row * token_stride + head * head_stride + d;
-  float x[2][8];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
-    if (mine) load8<F32, VEC>(kv ? v : k, from, x[kv]);
-  const long long at = first + ((long long)head << c.page_log2);
+  for (int i = 0; i < PER; ++i) {
+    const int e = e0 + i * kItem, head = head_of(e, inverse), d = e - head * c.head_dim;
+    const bool mine = e < width;
+    const long long at = first + ((long long)head << c.page_log2);
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    uint32_t w[4], s = 0;
-    if constexpr (FMT == kBf16) {
+    for (int kv = 0; kv < 2; ++kv) {
+      uint32_t w[4], s = 0;
+      float x[8];
+      values8<F32>(in[i][kv], x);
+      if constexpr (FMT == kBf16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(x[kv][2 * i], x[kv][2 * i + 1]);
-    } else {
-      uint32_t amax = 0;
-      if (mine) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[kv][i]) & 0x7FFFFFFFu);
-      }
-      amax = max(amax, __shfl_xor_sync(~0u, amax, 1));
-      amax = max(amax, __shfl_xor_sync(~0u, amax, 2));
-      s = scale_byte<FMT>(amax);
-      const float f = scale_inverse(s);
-      float u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = s == 255u ? 0.f : x[kv][i] * f;
-      if constexpr (FMT == kFp8) {
-        w[0] = pack_e4m3x4(u[0], u[1], u[2], u[3]);
-        w[1] = pack_e4m3x4(u[4], u[5], u[6], u[7]);
+        for (int y = 0; y < 4; ++y) w[y] = F32 ? pack_bf16x2(x[2 * y], x[2 * y + 1]) : in[i][kv][y];
       } else {
-        // The shuffle (of a lane's own word) keeps the compiler from folding the unpacking of the values
-        // below into this packing: nvcc 12.9 then loses the word's upper bytes.
-        w[0] = __shfl_sync(~0u, pack_e2m1x8(u), threadIdx.x & 31);
+        uint32_t amax = mine ? amax8<F32>(in[i][kv]) : 0u;
+        amax = max(amax, __shfl_xor_sync(~0u, amax, 1));
+        amax = max(amax, __shfl_xor_sync(~0u, amax, 2));
+        s = scale_byte<FMT>(amax);
+        const float f = scale_inverse(s);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) x[y] *= f;
+        if constexpr (FMT == kFp8) {
+          w[0] = s == 255u ? 0u : pack_e4m3x4(x[0], x[1], x[2], x[3]);
+          w[1] = s == 255u ? 0u : pack_e4m3x4(x[4], x[5], x[6], x[7]);
+        } else {
+          // The shuffle (of a lane's own word) keeps the compiler from folding the unpacking of the values
+          // below into this packing: nvcc 12.9 then loses the word's upper bytes.
+          w[0] = __shfl_sync(~0u, s == 255u ? 0u : pack_e2m1x8(x), threadIdx.x & 31);
+        }
+        if (mine && (threadIdx.x & 3) == 0) c.scales[kv][at * (c.head_dim / kGroup) + d / kGroup] = (unsigned char)s;
       }
-      if (mine && (threadIdx.x & 3) == 0) c.scales[kv][at * (c.head_dim / kGroup) + d / kGroup] = (unsigned char)s;
-    }
-    if (mine) {
-      store_codes<FMT>(c.pages[kv] + (at * c.head_dim + d) * code_bits(FMT) / 8, w);
-      void* out = kv ? v_values : k_values;
-      if (out) {
-        float y[8];
-        decode8<FMT>(w, s, y);
-        store8<F32, true>(out, (long long)row * width + e, y);
+      if (mine) {
+        store_codes<FMT>(c.pages[kv] + (at * c.head_dim + d) * code_bits(FMT) / 8, w);
+        void* out = kv ? v_values : k_values;
+        if (out) {
+          float y[8];
+          decode8<FMT>(w, s, y);
+          store8<F32, true>(out, (long long)row * width + e, y);
+        }
       }
     }
   }
 }
 
-template <int FMT, bool F32, bool VEC>
+template <int FMT, bool F32, bool VEC, int PER>
 __global__ void __launch_bounds__(kThreads) read_kernel(const Cache c, const Batch b, void* k, void* v,
                                                         long long token_stride, long long head_stride,
-                                                        unsigned int* status, int items) {
-  const long long item = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  const int row = (int)(item / items);
+                                                        unsigned int* status, int items, uint32_t inverse) {
+  const long long unit = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int row = (int)(unit / items);
   if (row >= b.n_rows) return;
-  const int e = (int)(item % items) * kItem + (threadIdx.x & 31) * 8;
+  const int e0 = (int)(unit % items) * (PER * kItem) + (threadIdx.x & 31) * 8, width = c.heads * c.head_dim;
   bool owned;
   const long long first = place_of(c, b, row, status, &owned);
-  if (!owned || e >= c.heads * c.head_dim) return;
-  const int head = e / c.head_dim, d = e % c.head_dim;
-  const long long at = first + ((long long)head << c.page_log2);
-  uint32_t w[2][4] = {}, s[2] = {};
-  if (first >= 0) {
+  if (!owned) return;
+  uint32_t w[PER][2][4] = {}, s[PER][2] = {};
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      load_codes<FMT>(c.pages[kv] + (at * c.head_dim + d) * code_bits(FMT) / 8, w[kv]);
-      if constexpr (FMT != kBf16) s[kv] = c.scales[kv][at * (c.head_dim / kGroup) + d / kGroup];
+  for (int i = 0; i < PER; ++i) {
+    const int e = e0 + i * kItem, head = head_of(e, inverse), d = e - head * c.head_dim;
+    const long long at = first + ((long long)head << c.page_log2);
+    if (first >= 0 && e < width) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        load_codes<FMT>(c.pages[kv] + (at * c.head_dim + d) * code_bits(FMT) / 8, w[i][kv]);
+        if constexpr (FMT != kBf16) s[i][kv] = c.scales[kv][at * (c.head_dim / kGroup) + d / kGroup];
+      }
     }
   }
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    float x[8];
-    decode8<FMT>(w[kv], s[kv], x);
-    store8<F32, VEC>(kv ? v : k, row * token_stride + head * head_stride + d, x);
+  for (int i = 0; i < PER; ++i) {
+    const int e = e0 + i * kItem;
+    if (e >= width) break;
+    const int head = head_of(e, inverse);
+    const long long to = row * token_stride + head * head_stride + (e - head * c.head_dim);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      float x[8];
+      decode8<FMT>(w[i][kv], s[i][kv], x);
+      store8<F32, VEC>(kv ? v : k, to, x);
+    }
   }
 }
 
@@ -207,42 +236,60 @@ bool wide(bool f32, const void* k, const void* v, long long token_stride, long l
   return ((uintptr_t)k | (uintptr_t)v) % 16 == 0 && token_stride % per == 0 && head_stride % per == 0;
 }
 
+// Warps for all rows, and whether there are enough for several items each.
+struct Grid {
+  uint32_t inverse;
+  int items;
+  unsigned blocks;
+  bool many;
+};
+Grid grid_of(const Cache& c, const Batch& b, int many) {
+  const int one = (c.heads * c.head_dim + kItem - 1) / kItem;
+  Grid g;
+  g.inverse = (uint32_t)(((1ull << 32) + c.head_dim - 1) / c.head_dim);
+  g.many = one > 1 && (long long)b.n_rows * one >= 148 * 64;   // a full GPU of warps with one item each
+  g.items = g.many ? (one + many - 1) / many : one;
+  g.blocks = (unsigned)(((long long)b.n_rows * g.items + kThreads / 32 - 1) / (kThreads / 32));
+  return g;
+}
+
 }  // namespace
+
+#define TACTKV_PER(FMT, F32, VEC, MANY) (g.many ? TACTKV_GO(FMT, F32, VEC, MANY) : TACTKV_GO(FMT, F32, VEC, 1))
+#define TACTKV_IO(FMT, MANY)                                                       \
+  (f32 ? (vec ? TACTKV_PER(FMT, true, true, MANY) : TACTKV_PER(FMT, true, false, MANY))  \
+       : (vec ? TACTKV_PER(FMT, false, true, MANY) : TACTKV_PER(FMT, false, false, MANY)))
 
 cudaError_t launch_append(int fmt, bool f32, const Cache& c, const Batch& b, const void* k, const void* v,
                           long long token_stride, long long head_stride, void* k_values, void* v_values,
                           unsigned int* status, cudaStream_t st) {
-  const int items = (c.heads * c.head_dim + kItem - 1) / kItem;
-  const long long blocks = ((long long)b.n_rows * items + kThreads / 32 - 1) / (kThreads / 32);
+  const Grid g = grid_of(c, b, 2);
   const bool vec = wide(f32, k, v, token_stride, head_stride);
-#define TACTKV_GO(FMT, F32, VEC)                                                                               \
-  append_kernel<FMT, F32, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(c, b, k, v, token_stride, head_stride,   \
-                                                                      k_values, v_values, status, items)
-#define TACTKV_IO(FMT)                                              \
-  (f32 ? (vec ? TACTKV_GO(FMT, true, true) : TACTKV_GO(FMT, true, false)) \
-       : (vec ? TACTKV_GO(FMT, false, true) : TACTKV_GO(FMT, false, false)))
-  if (fmt == kBf16) TACTKV_IO(kBf16);
-  else if (fmt == kFp8) TACTKV_IO(kFp8);
-  else TACTKV_IO(kFp4);
+#define TACTKV_GO(FMT, F32, VEC, PER)                                                                             \
+  append_kernel<FMT, F32, VEC, PER><<<g.blocks, kThreads, 0, st>>>(c, b, k, v, token_stride, head_stride, k_values, \
+                                                                   v_values, status, g.items, g.inverse)
+  if (fmt == kBf16) TACTKV_IO(kBf16, 2);
+  else if (fmt == kFp8) TACTKV_IO(kFp8, 2);
+  else TACTKV_IO(kFp4, 2);
 #undef TACTKV_GO
   return cudaGetLastError();
 }
 
 cudaError_t launch_read(int fmt, bool f32, const Cache& c, const Batch& b, void* k, void* v, long long token_stride,
                         long long head_stride, unsigned int* status, cudaStream_t st) {
-  const int items = (c.heads * c.head_dim + kItem - 1) / kItem;
-  const long long blocks = ((long long)b.n_rows * items + kThreads / 32 - 1) / (kThreads / 32);
+  const Grid g = grid_of(c, b, 4);
   const bool vec = wide(f32, k, v, token_stride, head_stride);
-#define TACTKV_GO(FMT, F32, VEC)                                                                             \
-  read_kernel<FMT, F32, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(c, b, k, v, token_stride, head_stride,   \
-                                                                    status, items)
-  if (fmt == kBf16) TACTKV_IO(kBf16);
-  else if (fmt == kFp8) TACTKV_IO(kFp8);
-  else TACTKV_IO(kFp4);
+#define TACTKV_GO(FMT, F32, VEC, PER)                                                                      \
+  read_kernel<FMT, F32, VEC, PER><<<g.blocks, kThreads, 0, st>>>(c, b, k, v, token_stride, head_stride,    \
+                                                                 status, g.items, g.inverse)
+  if (fmt == kBf16) TACTKV_IO(kBf16, 4);
+  else if (fmt == kFp8) TACTKV_IO(kFp8, 4);
+  else TACTKV_IO(kFp4, 4);
 #undef TACTKV_GO
-#undef TACTKV_IO
   return cudaGetLastError();
 }
+#undef TACTKV_IO
+#undef TACTKV_PER
 
 }  // namespace text
 }  // namespace tactkv
