@@ -205,46 +205,46 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   const int page_tokens = 1 << a.c.page_log2, run = min(page_tokens, Sh::kPart), runs = TT / run, of_part = Sh::kPart / run;
   bool copies_ok = true;
   int last_copy[2] = {-1, -1};                     // of K's and V's tiles
-      long long at = 0, at_next = 0;                 // the lane's run of this V's and the next K's tile
-      uint32_t good = 0, good_next = 0;              // the lanes whose runs are there
-      auto find = [&](int i) {                       // a lane copies a run of tokens, which never leaves its page
-        const int t = t0 + i * TT + lane * run;
-        const bool there = lane < runs && t < sp.len;
-        const int page = there ? __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2)) : -1;
-        const bool in = there && page >= 0 && page < a.c.n_pages;
-        if (there && !in) report(a.status);
-        const uint32_t bad = __reduce_or_sync(~0u, there && !in ? ((1u << run / 16) - 1) << (lane * run / 16) : 0u);
-        if (lane == 0) absent_of[i & 15] = bad;
-        good_next = __ballot_sync(~0u, in);
-        at_next = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & (page_tokens - 1));
-      };
-      auto copy = [&](int kv, int i) {
-        const long long from = kv ? at : at_next;
-        const uint32_t mask = kv ? good : good_next;
-        for (int half = 0; half < Sh::kParts && copies_ok; ++half) {
-          const int slot = slot_of(i, kv, half), round = round_of(i, kv);
-          if (round) copies_ok = wait(&bars->slot_free[slot], (round - 1) & 1, dead);
-          copies_ok = __all_sync(~0u, copies_ok);
-          if (!copies_ok) break;
-          const int mine = __popc(mask >> (half * of_part) & ((2u << (of_part - 1)) - 1));
-          if (lane == 0) tc::mbar_expect_tx(&bars->slot_full[slot], mine * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
-          last_copy[kv] = i;
-          __syncwarp();
-          if ((mask >> lane & 1) && lane / of_part == half) {
-            unsigned char* to = slots + slot * Sh::kSlot;
-            const int in = lane % of_part * run;      // the run's place in the slot
-            if constexpr (kCoded) {
-              tc::bulk_load(to + in * Sh::kRow, a.c.pages[kv] + from * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
-              tc::bulk_load(to + Sh::kRaw + in * (D / kGroup), a.c.scales[kv] + from * (D / kGroup), run * (D / kGroup),
-                            &bars->slot_full[slot]);
-            } else {
-  #pragma unroll
-              for (int b = 0; b < Sh::kBlocks; ++b)
-                tc::tma_load_2d(to + b * Sh::kBlock + in * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)from);
-            }
-          }
+  long long at = 0, at_next = 0;                 // the lane's run of this V's and the next K's tile
+  uint32_t good = 0, good_next = 0;              // the lanes whose runs are there
+  auto find = [&](int i) {                       // a lane copies a run of tokens, which never leaves its page
+    const int t = t0 + i * TT + lane * run;
+    const bool there = lane < runs && t < sp.len;
+    const int page = there ? __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2)) : -1;
+    const bool in = there && page >= 0 && page < a.c.n_pages;
+    if (there && !in) report(a.status);
+    const uint32_t bad = __reduce_or_sync(~0u, there && !in ? ((1u << run / 16) - 1) << (lane * run / 16) : 0u);
+    if (lane == 0) absent_of[i & 15] = bad;
+    good_next = __ballot_sync(~0u, in);
+    at_next = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & (page_tokens - 1));
+  };
+  auto copy = [&](int kv, int i) {
+    const long long from = kv ? at : at_next;
+    const uint32_t mask = kv ? good : good_next;
+    for (int half = 0; half < Sh::kParts && copies_ok; ++half) {
+      const int slot = slot_of(i, kv, half), round = round_of(i, kv);
+      if (round) copies_ok = wait(&bars->slot_free[slot], (round - 1) & 1, dead);
+      copies_ok = __all_sync(~0u, copies_ok);
+      if (!copies_ok) break;
+      const int mine = __popc(mask >> (half * of_part) & ((2u << (of_part - 1)) - 1));
+      if (lane == 0) tc::mbar_expect_tx(&bars->slot_full[slot], mine * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
+      last_copy[kv] = i;
+      __syncwarp();
+      if ((mask >> lane & 1) && lane / of_part == half) {
+        unsigned char* to = slots + slot * Sh::kSlot;
+        const int in = lane % of_part * run;      // the run's place in the slot
+        if constexpr (kCoded) {
+          tc::bulk_load(to + in * Sh::kRow, a.c.pages[kv] + from * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
+          tc::bulk_load(to + Sh::kRaw + in * (D / kGroup), a.c.scales[kv] + from * (D / kGroup), run * (D / kGroup),
+                        &bars->slot_full[slot]);
+        } else {
+#pragma unroll
+          for (int b = 0; b < Sh::kBlocks; ++b)
+            tc::tma_load_2d(to + b * Sh::kBlock + in * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)from);
         }
-      };
+      }
+    }
+  };
 
   // ---- set up: barriers and the first copy, tensor memory, the queries' operand ----
   constexpr int kProducer = 4 * Sh::kWGs, kIssuer = kProducer + 1;
@@ -343,11 +343,12 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       }
       if (copies_ok && !(kCoded && i == 0)) copy(1, i);
     }
-    // Copies in flight when a wait expired land before the block ends.
-    if (!copies_ok)
-      for (int kv = 0; kv < 2; ++kv)
-        for (int i = max(0, last_copy[kv] - kRing + 1); i <= last_copy[kv]; ++i)
-          for (int half = 0; half < Sh::kParts; ++half) wait(&bars->slot_full[slot_of(i, kv, half)], round_of(i, kv) & 1, nullptr);
+    // No copy is in flight when the block ends, not even one whose readers gave up.
+    for (int kv = 0; kv < 2; ++kv) {
+      const int newest = kCoded ? last_copy[kv] : max(turn_of(last_copy[0], 0), last_copy[1] < 0 ? 0 : turn_of(last_copy[1], 1));
+      for (int i = last_copy[kv]; i >= 0 && turn_of(i, kv) + kRing > newest; --i)
+        for (int half = 0; half < Sh::kParts; ++half) wait<true>(&bars->slot_full[slot_of(i, kv, half)], round_of(i, kv) & 1, nullptr);
+    }
   } else if (warp == kIssuer) {
     // -------------------------------------------------------------------------------- issuer ---
     if (lane == 0) {
@@ -394,8 +395,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
           for (int k = 0; k < TT / 16; ++k)
             tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16, p_desc + (i % Sh::kPs * Sh::kP + k * (16 * N * 2)) / 16,
                          kIdO, i > 0 || k > 0);
-        tc::mma_commit(&bars->pv_done[i & 1]);
         release(i, 1);
+        tc::mma_commit(&bars->pv_done[i & 1]);      // last: whoever sees it knows that every other arrival is in
       }
       if (!ok) {                                   // products in flight end before tensor memory is released
         tc::mma_commit(&bars->drain);

@@ -29,6 +29,8 @@ if torch.cuda.is_available():
 
 DEV = "cuda:0"
 FMTS = ["bf16", "mxfp8", "mxfp4"]
+# Calls bounded to 128 tokens and longer ones take different kernels (bfloat16 queries, head_dim 64, 128, 192, 256).
+BOUNDS = [None, 2000]
 IO = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
@@ -294,11 +296,12 @@ def test_attention_wide_trees(fmt, io, D, G, rows):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("prior", [False, True])
 @pytest.mark.parametrize("rows", [3, 40])
-def test_rows_that_see_nothing(fmt, prior, rows):
+@pytest.mark.parametrize("bound", BOUNDS)
+def test_rows_that_see_nothing(fmt, prior, rows, bound):
     s = Setup(fmt, 2, 64, 16, [(rows, rows), (2, 20)], seed=8)
     words = torch.zeros(rows + 2, dtype=torch.int64, device=DEV)
     words[1] = 1
-    out, m, l = check_attention(s, 8, "bf16", tree=words, prior=prior)
+    out, m, l = check_attention(s, 8, "bf16", tree=words, prior=prior, max_kv_len=bound)
     if not prior:
         assert not out[0].any() and torch.isneginf(m[0]).all() and not l[0].any()
         assert not out[rows - 1].any()
@@ -307,10 +310,11 @@ def test_rows_that_see_nothing(fmt, prior, rows):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", [6, 50])
-def test_infinities_and_nan_reach_only_the_rows_that_see_them(fmt, io, rows):
+@pytest.mark.parametrize("D,before,bound", [(64, 45, None), (64, 45, 2000), (128, 45, 2000), (256, 700, None), (192, 250, None)])
+def test_infinities_and_nan_reach_only_the_rows_that_see_them(fmt, io, rows, D, before, bound):
     """K and V of drafted tokens, and whatever stands behind the last token, hold infinities and NaN."""
-    s = Setup(fmt, 1, 64, 32, [(rows, 45 + rows), (rows, 31 + rows)], seed=4)
-    k, v = (torch.randn((2 * rows, 1, 64)) for _ in range(2))
+    s = Setup(fmt, 1, D, 32, [(rows, before + rows), (rows, 31 + rows)], seed=4)
+    k, v = (torch.randn((2 * rows, 1, D)) for _ in range(2))
     k[2, 0, 5], v[3, 0, 40], v[4, 0, 0] = math.nan, math.inf, math.nan
     T.text_append(s.cache, k.to(DEV), v.to(DEV), *s.batch, check=True)
     for i, (_, t) in enumerate(s.seqs):                   # the rest of the last page
@@ -322,23 +326,26 @@ def test_infinities_and_nan_reach_only_the_rows_that_see_them(fmt, io, rows):
             s.cache.v_scales[page, :, off:] = 255
     words = [1 << j for j in range(rows)]                 # every row sees itself alone
     words[5] |= 1 << 0
-    out, m, l = check_attention(s, 4, io, tree=torch.tensor(words * 2, dtype=torch.int64, device=DEV))
+    out, m, l = check_attention(s, 4, io, tree=torch.tensor(words * 2, dtype=torch.int64, device=DEV),
+                                max_kv_len=bound)
     assert torch.isnan(out[2]).all() and torch.isfinite(out[[0, 1, 5]]).all()
     assert not torch.isfinite(out[3, :, 40]).any() and torch.isnan(out[4, :, 0]).all()
     if fmt == "bf16":
         assert torch.isfinite(out[3, :, :40]).all() and torch.isfinite(out[4, :, 1:]).all()
     else:                                                 # the group reads back as NaN, the others as they were
         assert torch.isfinite(out[3, :, :32]).all() and torch.isfinite(out[4, :, 32:]).all()
+        assert torch.isfinite(out[3, :, 64:]).all()
     assert torch.isfinite(out[rows:rows + 2]).all()
 
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("scale,q_scale", [(1e-20, 1e18), (3e4, 1e-4), (1.0, 20.0), (1e15, 1e-17)])
-def test_far_ranges(fmt, scale, q_scale):
+@pytest.mark.parametrize("bound", BOUNDS)
+def test_far_ranges(fmt, scale, q_scale, bound):
     """K and V, and the queries against them, far from 1; and scores sharp enough for a one-hot softmax."""
     s = Setup(fmt, 2, 64, 16, [(4, 90), (1, 33)], seed=2, scale=scale)
-    check_attention(s, 2, "bf16", q_scale=q_scale)
-    check_attention(s, 2, "f32", q_scale=q_scale)
+    check_attention(s, 2, "bf16", q_scale=q_scale, max_kv_len=bound)
+    check_attention(s, 2, "f32", q_scale=q_scale, max_kv_len=bound)
 
 
 def test_scales_of_very_different_size_in_one_sequence():
@@ -372,35 +379,66 @@ def test_offsets_beyond_32_bits():
     assert ((out[0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -15) * mag).all()
 
 
-def test_attention_reports_bad_rows_and_pages():
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("before", [0, 640])
+def test_attention_reports_bad_rows_and_pages(fmt, before):
+    """Rows that do not fit see no text token, a bad page's tokens are left out, other sequences are as ever.  (before:
+    so many more tokens in front, for the kernel of long sequences.)"""
     heads, D = 1, 64
     for bad in ("page", "length", "rows", "max_len", "none"):
-        s = Setup("bf16", heads, D, 16, [(2, 40), (1, 20)], seed=1)
-        table, lens, max_rows, max_len = s.batch[0].clone(), s.batch[1].clone(), 2, 48
+        s = Setup(fmt, heads, D, 16, [(2, before + 40), (1, before + 20)], seed=1)
+        table, lens, max_rows, max_len = s.batch[0].clone(), s.batch[1].clone(), 2, before + 48
         if bad == "page":
             table[0, 1] = s.cache.n_pages
+            table[0, before // 16] = -5
         elif bad == "length":
             lens[0] = 1
         elif bad == "rows":
             max_rows = 1
         elif bad == "max_len":
-            max_len = 39
+            max_len = before + 39
         q = torch.randn((3, 2, D), device=DEV).bfloat16()
-        ws = T.text_workspace(s.cache, n_seqs=2, n_rows=3, max_rows=2, q_heads=2, max_kv_len=48)
+        ws = T.text_workspace(s.cache, n_seqs=2, n_rows=3, max_rows=2, q_heads=2, max_kv_len=before + 48)
         out, m, l = T.text_attention(q, s.cache, table, lens, s.batch[2], max_rows=max_rows, max_kv_len=max_len, workspace=ws)
         assert T.tactkv_device_status(ws.data_ptr(), ws.numel(), 0) == (T.TACTKV_OK if bad == "none" else T.TACTKV_INVALID_ARG)
-        ref = T.text_attention(q, s.cache, *s.batch, max_rows=2, max_kv_len=48)
+        ref = T.text_attention(q, s.cache, *s.batch, max_rows=2, max_kv_len=before + 48)
         assert torch.equal(out[2], ref[0][2])             # the other sequence
         if bad == "none":
             assert torch.equal(out, ref[0])
-        elif bad == "page":                               # the tokens 16 .. 31 are left out
+        elif bad == "page":                               # two pages' tokens are left out
             K, V = s.values()[0]
-            seen = P.visible(2, 40, None)
+            seen = P.visible(2, before + 40, None)
             seen[:, 16:32] = False
-            o, _, rl, _, S = P.attend(q[:2].double().cpu().numpy(), K, V, seen)
-            assert np.all(np.abs(l[:2].cpu().numpy() - rl) <= (2 * (D / 16 + 4) * 2.0 ** -23 * S + 2.0 ** -16) * rl)
+            seen[:, before:before + 16] = False
+            o, _, rl, mag, S = P.attend(q[:2].double().cpu().numpy(), K, V, seen)
+            dz = (D / 16 + 4) * 2.0 ** -23 * S
+            assert np.all(np.abs(l[:2].cpu().numpy() - rl) <= (2 * dz + 2.0 ** -16) * rl)
+            tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2 * dz + 2.0 ** -16)[..., None] * mag + 2.0 ** -22 * np.max(np.abs(V))
+            assert np.all(np.abs(out[:2].double().cpu().numpy() - o) <= tol)
         else:
             assert not out[:2].any() and torch.isneginf(m[:2]).all() and not l[:2].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,G,rows,page", [(64, 2, 5, 16), (128, 4, 4, 256), (128, 8, 9, 64), (192, 5, 4, 32), (256, 4, 4, 128)])
+def test_long_sequences_in_parts(fmt, D, G, rows, page):
+    """Sequences that are split over blocks, ragged, beside short ones; the same bits every time."""
+    s = Setup(fmt, 2, D, page, [(rows, 6000), (1, 1), (rows, 2900), (2, 129), (0, 50), (rows, 300)], seed=D + page, extra_rows=2)
+    first = check_attention(s, G, "bf16", tree="random", prior=True)
+    q = torch.randn((s.n_rows, 2 * G, D), device=DEV).bfloat16()
+    runs = [T.text_attention(q, s.cache, *s.batch, max_rows=rows, out=torch.zeros_like(q)) for _ in range(4)]
+    assert first[0].shape == q.shape
+    for r in runs[1:]:
+        end = s.starts()[-1]
+        assert all(torch.equal(a[:end], b[:end]) for a, b in zip(runs[0], r))
+
+
+def test_many_sequences():
+    """More sequences than blocks fit the GPU at once, lengths from 1 to 700, and one row each."""
+    lens = [1 + (i * 37) % 700 for i in range(500)]
+    for fmt in FMTS:
+        s = Setup(fmt, 1, 64, 64, [(1, t) for t in lens], seed=3, extra_rows=1)
+        check_attention(s, 4, "bf16", prior=True)
 
 
 # ------------------------------------------------------------------------------------- as it is used ---
@@ -439,6 +477,31 @@ def test_other_stream_and_captured_graph():
     s.seqs = [(1, 57), (3, 177)]
     s.batch = (table, lens, starts)
     verify(s, q.cpu(), None, None, want, "bf16")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_captured_graph_of_split_sequences(fmt):
+    """A captured call whose sequences are split over blocks, replayed on other lengths."""
+    s = Setup(fmt, 2, 128, 64, [(3, 3000), (2, 2500)], seed=2)
+    q = torch.randn((5, 8, 128), device=DEV).bfloat16()
+    table, lens, starts = (x.clone() for x in s.batch)
+    ws = T.text_workspace(s.cache, n_seqs=2, n_rows=5, max_rows=3, q_heads=8, max_kv_len=3008)
+    kw = dict(max_rows=3, max_kv_len=3008, workspace=ws)
+    T.text_attention(q, s.cache, table, lens, starts, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [T.text_attention(q, s.cache, table, lens, starts, **kw) for _ in range(3)]
+    for new in ([3000, 2500], [700, 2499], [129, 64]):
+        lens.copy_(ints(new))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [[x.clone() for x in g] for g in got]
+        want = T.text_attention(q, s.cache, table, lens, starts, **kw)
+        torch.cuda.synchronize()
+        for g in replayed:
+            assert all(torch.equal(a, b) for a, b in zip(want, g))
+    assert T.tactkv_device_status(ws.data_ptr(), ws.numel(), 0) == T.TACTKV_OK
 
 
 def test_two_calls_at_once():
