@@ -13,13 +13,13 @@
 namespace tactkv {
 namespace text {
 
-constexpr int kMaxParts = 4 * 148; // units times parts, where there is more than one part
-constexpr int kLeastPart = 256;    // tokens
+constexpr int kSms = 148;
+constexpr int kMaxParts = 4 * kSms;              // units times parts, where there is more than one part
+constexpr int kLeastPart = 256, kShortPart = 128, kFewParts = 16;   // tokens of a part; see plan()
 constexpr int kWideDim = 128;      // up to this head_dim a unit may have 32 rows (registers for their sums)
 
 constexpr int kPartRows(int D) { return D <= kWideDim ? 64 : 32; }
 
-constexpr int kSms = 148;
 // Up to one tile of text_tc.cu's the kernel of text_attention.cu is used: its start is shorter (128 tokens, 4 heads x 128,
 // 8 bits: 7.0 against 9.1 us; from 256 tokens on the other is, 9.6 against 10.1, 4096: 79 against 63).
 constexpr int kOneTile = 128;
@@ -146,12 +146,19 @@ __device__ __forceinline__ void finish_misfit(const AttnArgs& a, const Span& sp,
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
-// The split of a launch into at most `blocks` blocks, and each sequence into parts of at least `least` tokens.
-inline void plan(const AttnArgs& a, int tile_rows, int blocks, int least, Parts& p) {
+// The split of a launch into at most `blocks` blocks, and each sequence into parts, which have at least kLeastPart tokens:
+// with half of that the sum over more parts costs more than it gains (4000 tokens x 4 heads x 128, tcgen05: bfloat16 11.6
+// against 11.2 us, 8 bits 13.6 against 13.3; head_dim 96 on the other kernel: 17.7 against 13.7).  kShortPart is used where
+// it makes few parts (kFewParts) and no SM gets two: 1000 tokens 9.1 against 9.9 us, 12.1 against 13.2 (350 tokens, 4
+// sequences of 16 rows) and, on the other kernel, 9.7 against 11.8 and 17.3 against 22.8 (float32, head_dim 256).  Sequences
+// of up to `whole` tokens are not split.
+inline void plan(const AttnArgs& a, int tile_rows, int blocks, int whole, Parts& p) {
   p.tile_rows = tile_rows;
   p.tiles = (a.max_rows * (a.q_heads / a.c.heads) + tile_rows - 1) / tile_rows;
-  const long long units = (long long)a.b.n_seqs * a.c.heads * p.tiles, most = (a.max_len + least - 1) / least;
-  p.count = (int)std::max(1ll, std::min(most, blocks / units));
+  const long long units = (long long)a.b.n_seqs * a.c.heads * p.tiles, most = (a.max_len + kShortPart - 1) / kShortPart;
+  const bool shorts = a.max_len > whole && most <= kFewParts && units * most <= kSms;
+  const int least = shorts ? kShortPart : kLeastPart;
+  p.count = (int)std::max(1ll, std::min<long long>((a.max_len + least - 1) / least, blocks / units));
   p.tokens = std::max(least, ((a.max_len + p.count - 1) / p.count + 127) / 128 * 128);
   p.count = std::max(1, (a.max_len + p.tokens - 1) / p.tokens);
 }

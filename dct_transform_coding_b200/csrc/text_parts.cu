@@ -78,7 +78,7 @@ cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspa
 #undef TACTKV_CASE
     }
   } else {
-    plan(a, rows <= 8 ? 8 : (rows <= 16 || D > kWideDim ? 16 : 32), kMaxParts, kLeastPart, p);
+    plan(a, rows <= 8 ? 8 : (rows <= 16 || D > kWideDim ? 16 : 32), kMaxParts, kShortPart, p);
     switch (D) {
 #define TACTKV_CASE(D) case D: e = launch_parts_##D(fmt, f32, a, p, st); break;
       TACTKV_FOR_D(TACTKV_CASE)

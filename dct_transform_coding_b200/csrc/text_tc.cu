@@ -835,7 +835,7 @@ cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
   }
   CUtensorMap maps[2] = {};
   if (FMT == kBf16 && !(make_map(a, 0, &maps[0]) && make_map(a, 1, &maps[1]))) return cudaErrorInvalidValue;
-  plan(a, N, kSms * Sh::kCtas, 2 * TT, p);
+  plan(a, N, kSms * Sh::kCtas, 2 * TT, p);   // (two tiles: 8.3 us whole, 9.2 in parts)
   tc_kernel<FMT, N><<<dim3(p.count, a.c.heads * p.tiles, a.b.n_seqs), Sh::kThreads, Sh::kSmem, st>>>(a, p, maps[0], maps[1]);
   return cudaGetLastError();
 }
