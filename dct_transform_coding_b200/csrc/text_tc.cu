@@ -202,46 +202,57 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   auto round_of = [&](int i, int kv) { return turn_of(i, kv) / kRing; };
 
   // ---- the producer's copies ----
-  const int page_tokens = 1 << a.c.page_log2, run = min(page_tokens, Sh::kPart), runs = TT / run, of_part = Sh::kPart / run;
+  // A lane copies a run of tokens, which never leaves its page; K's or V's two slots of a tile are filled at once.  (With
+  // quotients in the loop, a slot at a time and the page number read when it was needed, this warp's own chain was the
+  // kernel's bound: 3500 cycles a tile.)
+  const int page_tokens = 1 << a.c.page_log2, run = min(page_tokens, Sh::kPart), of_part = Sh::kPart / run;
+  const int my_half = lane / of_part, my_place = lane % of_part * run;
+  const uint32_t of_half = (2u << (of_part - 1)) - 1;
   bool copies_ok = true;
   int last_copy[2] = {-1, -1};                     // of K's and V's tiles
-  long long at = 0, at_next = 0;                 // the lane's run of this V's and the next K's tile
-  uint32_t good = 0, good_next = 0;              // the lanes whose runs are there
-  auto find = [&](int i) {                       // a lane copies a run of tokens, which never leaves its page
+  long long at = 0, at_next = 0;                   // the lane's run of this V's and the next K's tile
+  uint32_t good = 0, good_next = 0;                // the lanes whose runs are there
+  int page_ahead = -1;                             // of the lane's run in the tile after
+  auto look = [&](int i) {
     const int t = t0 + i * TT + lane * run;
-    const bool there = lane < runs && t < sp.len;
-    const int page = there ? __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2)) : -1;
-    const bool in = there && page >= 0 && page < a.c.n_pages;
-    if (there && !in) report(a.status);
-    const uint32_t bad = __reduce_or_sync(~0u, there && !in ? ((1u << run / 16) - 1) << (lane * run / 16) : 0u);
-    if (lane == 0) absent_of[i & 15] = bad;
+    page_ahead = my_half < Sh::kParts && t < sp.len ? __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2)) : -1;
+  };
+  auto find = [&](int i) {
+    const int t = t0 + i * TT + lane * run, page = page_ahead;
+    const bool there = my_half < Sh::kParts && t < sp.len, in = there && page >= 0 && page < a.c.n_pages;
+    if (i + 1 < n_tiles) look(i + 1);
     good_next = __ballot_sync(~0u, in);
+    uint32_t bad = __ballot_sync(~0u, there && !in);
+    if (bad) {                                     // 16 tokens to a bit
+      if (there && !in) report(a.status);
+      bad = __reduce_or_sync(~0u, there && !in ? ((1u << run / 16) - 1) << (lane * run / 16) : 0u);
+    }
+    if (lane == 0) absent_of[i & 15] = bad;
     at_next = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & (page_tokens - 1));
   };
   auto copy = [&](int kv, int i) {
     const long long from = kv ? at : at_next;
     const uint32_t mask = kv ? good : good_next;
-    for (int half = 0; half < Sh::kParts && copies_ok; ++half) {
-      const int slot = slot_of(i, kv, half), round = round_of(i, kv);
-      if (round) copies_ok = wait(&bars->slot_free[slot], (round - 1) & 1, dead);
-      copies_ok = __all_sync(~0u, copies_ok);
-      if (!copies_ok) break;
-      const int mine = __popc(mask >> (half * of_part) & ((2u << (of_part - 1)) - 1));
-      if (lane == 0) tc::mbar_expect_tx(&bars->slot_full[slot], mine * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
-      last_copy[kv] = i;
-      __syncwarp();
-      if ((mask >> lane & 1) && lane / of_part == half) {
-        unsigned char* to = slots + slot * Sh::kSlot;
-        const int in = lane % of_part * run;      // the run's place in the slot
-        if constexpr (kCoded) {
-          tc::bulk_load(to + in * Sh::kRow, a.c.pages[kv] + from * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
-          tc::bulk_load(to + Sh::kRaw + in * (D / kGroup), a.c.scales[kv] + from * (D / kGroup), run * (D / kGroup),
-                        &bars->slot_full[slot]);
-        } else {
+    const int round = round_of(i, kv);
+    if (round) copies_ok = wait(&bars->slot_free[slot_of(i, kv, lane % Sh::kParts)], (round - 1) & 1, dead);
+    copies_ok = __all_sync(~0u, copies_ok);
+    if (!copies_ok) return;
+    if (lane < Sh::kParts)
+      tc::mbar_expect_tx(&bars->slot_full[slot_of(i, kv, lane)],
+                         __popc(mask >> (lane * of_part) & of_half) * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
+    last_copy[kv] = i;
+    __syncwarp();
+    if (mask >> lane & 1) {
+      const int slot = slot_of(i, kv, my_half);
+      unsigned char* to = slots + slot * Sh::kSlot;
+      if constexpr (kCoded) {
+        tc::bulk_load(to + my_place * Sh::kRow, a.c.pages[kv] + from * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
+        tc::bulk_load(to + Sh::kRaw + my_place * (D / kGroup), a.c.scales[kv] + from * (D / kGroup), run * (D / kGroup),
+                      &bars->slot_full[slot]);
+      } else {
 #pragma unroll
-          for (int b = 0; b < Sh::kBlocks; ++b)
-            tc::tma_load_2d(to + b * Sh::kBlock + in * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)from);
-        }
+        for (int b = 0; b < Sh::kBlocks; ++b)
+          tc::tma_load_2d(to + b * Sh::kBlock + my_place * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)from);
       }
     }
   };
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   // ---- set up: barriers and the first copy, tensor memory, the queries' operand ----
   constexpr int kProducer = 4 * Sh::kWGs, kIssuer = kProducer + 1;
   if (warp == kProducer) {
-    find(0);
+    look(0);
     if (lane < Sh::kSlots) {
       tc::mbar_init(&bars->slot_full[lane], 1);
       tc::mbar_init(&bars->slot_free[lane], kCoded ? Sh::kDecoders / 4 : 1);
@@ -272,6 +283,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     }
     tc::fence_mbar_init();
     __syncwarp();
+    find(0);
     copy(0, 0);
     if constexpr (kCoded) {
       at = at_next, good = good_next;
