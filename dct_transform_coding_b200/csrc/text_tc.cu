@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   float2* row_fm = row_ml + N;                                            // a row's factor, its reference's negative
   float* exchange = reinterpret_cast<float*>(row_fm + N);                                            // [WG][warp][2 R]
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x & 31;   // (uniform for the compiler, too)
   const int G = a.q_heads / a.c.heads;
   const int part = blockIdx.x, seq = blockIdx.z, tiles = gridDim.y / a.c.heads;
   const int head = blockIdx.y / tiles, tile = blockIdx.y % tiles;
@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     }
   } else if (warp == kIssuer) {
     // -------------------------------------------------------------------------------- issuer ---
-    if (lane == 0) {
+    // The whole warp goes along, so that descriptors stay in uniform registers; one lane issues.
+    {
       constexpr uint32_t kIdS = kCoded ? tc::idesc_f16(128, N, false) : tc::idesc_bf16(128, N, false);
       constexpr uint32_t kIdO = (kCoded ? tc::idesc_f16(128, N, true) : tc::idesc_bf16(128, N, true)) | tc::kIdescBMn;
       // P is MN-major: a token's N rows are 32, 64 or 128 bytes with the swizzle of that width
@@ -374,8 +375,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         return tc::smem_u32(kCoded ? k_op + op(i, kv) * Sh::kOp : slots + slot_of(i, kv, 0) * Sh::kSlot);
       };
       auto full = [&](int i, int kv) {
-        return kCoded ? wait(&bars->op_full[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, dead)
-                      : wait(&bars->slot_full[slot_of(i, kv, 0)], round_of(i, kv) & 1, dead);
+        return __all_sync(~0u, kCoded ? wait(&bars->op_full[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, dead)
+                                      : wait(&bars->slot_full[slot_of(i, kv, 0)], round_of(i, kv) & 1, dead));
       };
       auto release = [&](int i, int kv) {
         tc::mma_commit(kCoded ? &bars->op_free[op(i, kv)] : &bars->slot_free[slot_of(i, kv, 0)]);
@@ -385,33 +386,39 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         if (!full(i, 0)) return false;
         tc::fence_after_sync();
         const uint64_t k_desc = tc::smem_desc(operand(i, 0), 16, 1024, 2);
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)           // addresses in descriptors count 16 bytes
-          tc::mma_bf16(tmem + (i & 1) * N, k_desc + (k / 4 * Sh::kBlock + k % 4 * 32) / 16,
-                       q_desc + (k / 4 * (N * 128) + k % 4 * 32) / 16, kIdS, k > 0);
-        tc::mma_commit(&bars->s_full[i & 1]);
-        release(i, 0);
+          for (int k = 0; k < D / 16; ++k)         // addresses in descriptors count 16 bytes
+            tc::mma_bf16(tmem + (i & 1) * N, k_desc + (k / 4 * Sh::kBlock + k % 4 * 32) / 16,
+                         q_desc + (k / 4 * (N * 128) + k % 4 * 32) / 16, kIdS, k > 0);
+          tc::mma_commit(&bars->s_full[i & 1]);
+          release(i, 0);
+        }
+        __syncwarp();
         return true;
       };
       bool ok = scores(0);
       for (int i = 0; i < n_tiles && ok; ++i) {
         if (i + 1 < n_tiles) ok = scores(i + 1);
         if (ok) ok = full(i, 1);
-        if (ok) ok = wait(&bars->p_full[i & 1], i / 2 & 1, dead);
+        if (ok) ok = __all_sync(~0u, wait(&bars->p_full[i & 1], i / 2 & 1, dead));
         if (!ok) break;
         tc::fence_after_sync();
         const uint64_t v_desc = tc::smem_desc(operand(i, 1), Sh::kBlock, 1024, 2);
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int g = 0; g < Sh::kGroups; ++g)
+          for (int g = 0; g < Sh::kGroups; ++g)
 #pragma unroll
-          for (int k = 0; k < TT / 16; ++k)
-            tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16, p_desc + (i % Sh::kPs * Sh::kP + k * (16 * N * 2)) / 16,
-                         kIdO, i > 0 || k > 0);
-        release(i, 1);
-        tc::mma_commit(&bars->pv_done[i & 1]);      // last: whoever sees it knows that every other arrival is in
+            for (int k = 0; k < TT / 16; ++k)
+              tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16, p_desc + (i % Sh::kPs * Sh::kP + k * (16 * N * 2)) / 16,
+                           kIdO, i > 0 || k > 0);
+          release(i, 1);
+          tc::mma_commit(&bars->pv_done[i & 1]);      // last: whoever sees it knows that every other arrival is in
+        }
+        __syncwarp();
       }
       if (!ok) {                                   // products in flight end before tensor memory is released
-        tc::mma_commit(&bars->drain);
+        if (tc::elect_one()) tc::mma_commit(&bars->drain);
         wait(&bars->drain, 0, nullptr);
       }
     }
