@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int kPad = kBlocks % 2 ? kBlock : 0;
   static constexpr int kRest = 1024 + kQ + kPs * kP + kFactors + kTops + kMisc + kPad;
   // Two blocks on an SM where two slots fit each: one's start, end and waits are the other's time.
-  static constexpr int kCtas = N <= (kCoded ? 16 : 32) && kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot <= 113 * 1024 ? 2 : 1;
+  static constexpr int kCtas = N <= (kCoded ? 16 : 32) && (!kCoded || D == 64) && kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot <= 113 * 1024 ? 2 : 1;
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;        // V operands in turn
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
   static constexpr int kDecoders = !kCoded ? 0 : (D > 128 ? 16 : 8);
@@ -234,25 +234,29 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     const long long from = kv ? at : at_next;
     const uint32_t mask = kv ? good : good_next;
     const int round = round_of(i, kv);
-    if (round) copies_ok = wait(&bars->slot_free[slot_of(i, kv, lane % Sh::kParts)], (round - 1) & 1, dead);
-    copies_ok = __all_sync(~0u, copies_ok);
-    if (!copies_ok) return;
-    if (lane < Sh::kParts)
-      tc::mbar_expect_tx(&bars->slot_full[slot_of(i, kv, lane)],
-                         __popc(mask >> (lane * of_part) & of_half) * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
-    last_copy[kv] = i;
-    __syncwarp();
-    if (mask >> lane & 1) {
-      const int slot = slot_of(i, kv, my_half);
-      unsigned char* to = slots + slot * Sh::kSlot;
-      if constexpr (kCoded) {
-        tc::bulk_load(to + my_place * Sh::kRow, a.c.pages[kv] + from * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
-        tc::bulk_load(to + Sh::kRaw + my_place * (D / kGroup), a.c.scales[kv] + from * (D / kGroup), run * (D / kGroup),
-                      &bars->slot_full[slot]);
-      } else {
+    constexpr int kAtOnce = kRing > 1 ? Sh::kParts : 1;   // (a lone slot's copy does not wait for the other half's)
 #pragma unroll
-        for (int b = 0; b < Sh::kBlocks; ++b)
-          tc::tma_load_2d(to + b * Sh::kBlock + my_place * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)from);
+    for (int first = 0; first < Sh::kParts; first += kAtOnce) {
+      if (round) copies_ok = wait(&bars->slot_free[slot_of(i, kv, first + lane % kAtOnce)], (round - 1) & 1, dead);
+      copies_ok = __all_sync(~0u, copies_ok);
+      if (!copies_ok) return;
+      if (lane < kAtOnce)
+        tc::mbar_expect_tx(&bars->slot_full[slot_of(i, kv, first + lane)],
+                           __popc(mask >> ((first + lane) * of_part) & of_half) * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
+      last_copy[kv] = i;
+      __syncwarp();
+      if ((mask >> lane & 1) && my_half >= first && my_half < first + kAtOnce) {
+        const int slot = slot_of(i, kv, my_half);
+        unsigned char* to = slots + slot * Sh::kSlot;
+        if constexpr (kCoded) {
+          tc::bulk_load(to + my_place * Sh::kRow, a.c.pages[kv] + from * Sh::kRow, run * Sh::kRow, &bars->slot_full[slot]);
+          tc::bulk_load(to + Sh::kRaw + my_place * (D / kGroup), a.c.scales[kv] + from * (D / kGroup), run * (D / kGroup),
+                        &bars->slot_full[slot]);
+        } else {
+#pragma unroll
+          for (int b = 0; b < Sh::kBlocks; ++b)
+            tc::tma_load_2d(to + b * Sh::kBlock + my_place * 128, kv ? &v_map : &k_map, &bars->slot_full[slot], 64 * b, (int)from);
+        }
       }
     }
   };
