@@ -122,6 +122,23 @@ __device__ float value_at(const Cache& c, int kv, long long at, int d) {
   return unpack2<true>(h[0]).x * f;
 }
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ unsigned long long bits2(float2 v) { return *reinterpret_cast<const unsigned long long*>(&v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(y) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return *reinterpret_cast<const float2*>(&y);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long y;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(y) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<const float2*>(&y);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long y;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(y) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<const float2*>(&y);
+}
 __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
@@ -176,8 +193,9 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   uint32_t* absent_of = reinterpret_cast<uint32_t*>(misc + 576);          // [tile % 16] 16-token blocks on bad pages
   unsigned long long* words = reinterpret_cast<unsigned long long*>(misc + 1024);
   float2* row_ml = reinterpret_cast<float2*>(words + N);
-  float2* row_fm = row_ml + N;                                            // a row's factor, its reference's negative
-  float* exchange = reinterpret_cast<float*>(row_fm + N);                                            // [WG][warp][2 R]
+  float* row_f = reinterpret_cast<float*>(row_ml + N);                    // a row's factor, its reference's negative
+  float* row_r = row_f + N;
+  float* exchange = row_r + N;                                            // [WG][warp][2 R]
 
   const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x & 31;   // (uniform for the compiler, too)
   const int G = a.q_heads / a.c.heads;
@@ -336,7 +354,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         *reinterpret_cast<uint32_t*>(q_op + d / 64 * (N * 128) + n * 128 + ((d % 64 / 8) ^ (n & 7)) * 16 + d % 8 * 2) = w[x][i];
       }
       if (lane == 0) {
-        row_fm[n] = make_float2(back, 0.f);
+        row_f[n] = back, row_r[n] = 0.f;
         words[n] = word[x];
       }
     }
@@ -455,9 +473,12 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       tc::tmem_ld<R>(lanes + (i & 1) * N + rows0, x);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int n = 0; n < R; n += 2) {             // the scores less the references
-        const float4 f = *reinterpret_cast<const float4*>(row_fm + rows0 + n);
-        x[n] = fmaf(x[n], k_scale * f.x, f.y), x[n + 1] = fmaf(x[n + 1], k_scale * f.z, f.w);
+      for (int n = 0; n < R; n += 4) {             // the scores less the references
+        const float4 f = *reinterpret_cast<const float4*>(row_f + rows0 + n), r = *reinterpret_cast<const float4*>(row_r + rows0 + n);
+        const float2 ks = make_float2(k_scale, k_scale);
+        const float2 a = fma2(make_float2(x[n], x[n + 1]), kCoded ? mul2(ks, make_float2(f.x, f.y)) : make_float2(f.x, f.y), make_float2(r.x, r.y));
+        const float2 b = fma2(make_float2(x[n + 2], x[n + 3]), kCoded ? mul2(ks, make_float2(f.z, f.w)) : make_float2(f.z, f.w), make_float2(r.z, r.w));
+        x[n] = a.x, x[n + 1] = a.y, x[n + 2] = b.x, x[n + 3] = b.y;
       }
       if (tail || bad) {
         const uint32_t* half = reinterpret_cast<const uint32_t*>(words + rows0) + (node >> 5 & 1);
@@ -502,7 +523,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
             if (moves) {
               shift = by;
               scale = first ? 0.f : exp2_fast(-by);
-              row_fm[rows0 + tid].y -= by;
+              row_r[rows0 + tid] -= by;
             }
           }
           const uint32_t moved = __ballot_sync(~0u, moves);
@@ -545,8 +566,10 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       for (int n = 0; n < R; n += 2) {
         const float p0 = exp2_fast(x[n]), p1 = exp2_fast(x[n + 1]);
         high[n] = fmaxf(high[n], x[n]), high[n + 1] = fmaxf(high[n + 1], x[n + 1]);
-        l[n] += p0, l[n + 1] += p1;
-        w[n / 2] = pack2<kCoded>(kCoded ? p0 * fold : p0, kCoded ? p1 * fold : p1);
+        const float2 p = make_float2(p0, p1), sum = add2(make_float2(l[n], l[n + 1]), p);
+        l[n] = sum.x, l[n + 1] = sum.y;
+        const float2 y = kCoded ? mul2(p, make_float2(fold, fold)) : p;
+        w[n / 2] = pack2<kCoded>(y.x, y.y);
       }
       if (i >= Sh::kPs) ok = wait(&bars->pv_done[(i - Sh::kPs) & 1], (i - Sh::kPs) / 2 & 1, dead);   // P's place is free
       ok = __all_sync(~0u, ok);
@@ -617,8 +640,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
           sum += exchange[(wg * 4 + w) * 2 * R + R + tid];
         }
         const float to = m == -INFINITY ? 0.f : exp2f(-m);
-        row_ml[rows0 + tid] = make_float2(m == -INFINITY ? m : m - row_fm[rows0 + tid].y, sum * to);
-        row_fm[rows0 + tid].x = to * (kCoded ? scale_value(ref) * 0.015625f : 1.f);   // of the row's sums
+        row_ml[rows0 + tid] = make_float2(m == -INFINITY ? m : m - row_r[rows0 + tid], sum * to);
+        row_f[rows0 + tid] = to * (kCoded ? scale_value(ref) * 0.015625f : 1.f);   // of the row's sums
       }
       bar_sync(bar);
       float* sums = reinterpret_cast<float*>(kCoded ? smem : slots);
@@ -629,7 +652,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         tc::tmem_ld_wait();
         if (g * 128 + tid < D) {
 #pragma unroll
-          for (int n = 0; n < R; ++n) sums[(rows0 + n) * (D + 4) + g * 128 + tid] = o[n] * row_fm[rows0 + n].x;
+          for (int n = 0; n < R; ++n) sums[(rows0 + n) * (D + 4) + g * 128 + tid] = o[n] * row_f[rows0 + n];
         }
       }
       // Infinities and NaN of drafted tokens, for the rows that see them (rare): p by one thread a row.
