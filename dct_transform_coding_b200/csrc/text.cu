@@ -65,6 +65,17 @@ tactkv_status check_rows(const void* k, const void* v, int64_t token_stride, int
 // Rows whose launch would not fit a grid's x dimension.
 bool too_many(const Batch& b, long long per_row) { return (long long)b.n_rows * per_row > INT_MAX; }
 
+// Whether (row, head) places of head_dim elements can be written without one meeting another: the outer of the two
+// strides passes all that the inner one spans.
+bool disjoint(const Cache& c, const Batch& b, int64_t token_stride, int64_t head_stride) {
+  const int64_t rows = b.n_rows, heads = c.heads, by_head = head_stride < 0 ? -head_stride : head_stride;
+  if (rows == 1 || heads == 1) return (rows == 1 || token_stride >= c.head_dim) && (heads == 1 || by_head >= c.head_dim);
+  const bool token_major = by_head < token_stride;
+  const int64_t inner = token_major ? by_head : token_stride, outer = token_major ? token_stride : by_head;
+  const int64_t n = token_major ? heads : rows;
+  return inner >= c.head_dim && inner <= (INT64_MAX - c.head_dim) / n && outer >= (n - 1) * inner + c.head_dim;
+}
+
 }  // namespace
 }  // namespace text
 }  // namespace tactkv
@@ -111,6 +122,7 @@ tactkv_status tactkv_text_read(const tactkv_text_cache* cache, const tactkv_text
   st = check_rows(k, v, token_stride, head_stride, flags);
   if (st != TACTKV_OK) return st;
   if (too_many(b, (c.heads * c.head_dim + 255) / 256)) return TACTKV_UNSUPPORTED_SHAPE;
+  if (!disjoint(c, b, token_stride, head_stride)) return TACTKV_INVALID_ARG;
   return launch_read(cache->format, flags & TACTKV_FP32_IO, c, b, k, v, token_stride, head_stride,
                      static_cast<unsigned int*>(workspace), stream) == cudaSuccess ? TACTKV_OK : TACTKV_CUDA;
 }
@@ -125,7 +137,11 @@ tactkv_status tactkv_text_attention(const tactkv_text_cache* cache, const tactkv
   tactkv_status st = check(cache, batch, flags, a.c, a.b);
   if (st != TACTKV_OK) return st;
   if (q_heads < 1 || max_rows < 1 || max_kv_len < 0) return TACTKV_INVALID_ARG;
-  if (max_rows > kMaxRows || max_kv_len > kMaxLen || a.b.n_seqs > 65535 || q_heads % a.c.heads || q_heads / a.c.heads > kMaxGroup) return TACTKV_UNSUPPORTED_SHAPE;
+  if (max_rows > kMaxRows || max_kv_len > kMaxLen || a.b.n_seqs > 65535 || q_heads % a.c.heads || q_heads / a.c.heads > kMaxGroup)
+    return TACTKV_UNSUPPORTED_SHAPE;
+  // TMA's coordinates are 32-bit (such a pool would be larger than the GPU's memory)
+  if (cache->format == TACTKV_TEXT_BF16 && ((long long)a.c.n_pages * a.c.heads << a.c.page_log2) > INT_MAX)
+    return TACTKV_UNSUPPORTED_SHAPE;
   st = check_workspace(workspace, workspace_bytes,
                        tactkv_text_workspace_bytes(cache, a.b.n_seqs, a.b.n_rows, q_heads, max_rows, max_kv_len));
   if (st != TACTKV_OK || !a.b.n_seqs || !a.b.n_rows) return st;

@@ -1,6 +1,7 @@
 // Attention over the text cache: what its kernels share (internal header).
 //
-// A launch splits every sequence into parts of `part` tokens (one part when the rows alone fill the GPU);
+// A launch splits every sequence into parts of Parts::tokens tokens (one part when the rows alone fill the GPU: 32 sequences x
+// 8 heads and 4 x 8 x 8 tiles of 64 rows both took longer in two parts than in one);
 // a part's (m, l, sum) goes to the workspace and the parts are summed by combine_kernel in their order,
 // so results do not depend on timing.  Scores are held as log2: z = s * log2(e).
 #pragma once

@@ -17,6 +17,10 @@ namespace {
 constexpr int kThreads = 128;
 
 // out, m and l of one (row, query head): its parts' sums, each to the largest maximum, in the parts' order.
+//   m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum o_i 2^(m_i - m) / l
+// A block takes one row; its threads take four columns each and every n-th part.  A read of the workspace, which is still in
+// the L2, bound by its latency: about 2 us of a call.  Its launch overlaps the end of the parts' kernel (1000 tokens, 4 heads
+// x 128: 9.8 against 10.6 us).
 template <bool F32>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, const Parts p) {
   __shared__ float4 sum[kThreads];

@@ -241,7 +241,8 @@ tactkv_status tactkv_attention_decode(const tactkv_unit* k_units, const tactkv_u
    row_starts[s+1]-1 (row_starts[0] = 0, not decreasing), n_s of them, which stand for the cache positions
    kv_lens[s] - n_s .. kv_lens[s] - 1: kv_lens counts the sequence's tokens with these rows among
    them.  Position t is token t % page_tokens of page page_table[s*max_pages + t / page_tokens].  Rows
-   from row_starts[n_seqs] on (a padded batch) are neither read nor written.  page_table, kv_lens and
+   from row_starts[n_seqs] on (a padded batch) have no effect, and their places in the outputs are left as they
+   are.  page_table, kv_lens and
    row_starts are DEVICE arrays of int32, read when the kernels run, so that a captured call can be
    replayed on other lengths and pages.  A page may be shared by sequences that only read it; a
    position that a call appends to must belong to one sequence alone.
@@ -249,7 +250,8 @@ tactkv_status tactkv_attention_decode(const tactkv_unit* k_units, const tactkv_u
    Errors found by the kernels are recorded as TACTKV_INVALID_ARG in the workspace (zeroed by the
    caller before its first use; tactkv_device_status): rows, lengths or tables that do not fit together
    (n_s < 0, kv_lens[s] < n_s, more tokens than max_pages pages hold or, for attention, than
-   max_kv_len, more rows than n_rows or max_rows) and page numbers outside 0 .. n_pages-1.  Nothing is
+   max_kv_len, more rows than n_rows or max_rows) and page numbers outside 0 .. n_pages-1.  (TACTKV_TIMEOUT
+   from tactkv_text_attention: a wait inside the kernel ran out, and its results are not whole.)  Nothing is
    read or written outside the arrays: append skips such rows, read zero-fills them, and attention
    leaves the tokens of such pages, or all tokens of such a sequence, out. */
 #define TACTKV_TEXT_BF16  0
@@ -291,7 +293,8 @@ tactkv_status tactkv_text_append(const tactkv_text_cache* cache, const tactkv_te
                                  struct CUstream_st* stream);
 
 /* Read the rows' K and V from the cache into k and v (indexed and typed as for append).  With n_s =
-   kv_lens[s] that is the whole sequence.  Asynchronous on `stream`; one kernel. */
+   kv_lens[s] that is the whole sequence.  Strides with which two (row, head) places would meet are
+   TACTKV_INVALID_ARG.  Asynchronous on `stream`; one kernel. */
 tactkv_status tactkv_text_read(const tactkv_text_cache* cache, const tactkv_text_batch* batch, void* k, void* v,
                                int64_t token_stride, int64_t head_stride, uint32_t flags, void* workspace,
                                size_t workspace_bytes, struct CUstream_st* stream);
@@ -299,8 +302,8 @@ tactkv_status tactkv_text_read(const tactkv_text_cache* cache, const tactkv_text
 /* Attention of the rows over their sequences' cached tokens: the rows are the last generated token
    (n_s = 1) or a tree of drafted tokens, appended before this call.
      q_heads     query heads, a multiple G of the cache's heads (G <= 16); query head j reads K/V head j/G;
-     max_rows    a bound on every n_s, 1 to 64; max_kv_len a bound on every kv_lens[s] (both size the launch
-                 and the workspace);
+     max_rows    a bound on every n_s, 1 to 64; max_kv_len a bound on every kv_lens[s], up to 2^30 (both size the
+                 launch: a closer bound is a faster call); n_seqs up to 65535, heads up to 1023;
      q           (row, head, d) at q + row*q_token_stride + head*q_head_stride + d: bfloat16, or float32
                  with TACTKV_FP32_IO; 16-byte aligned, strides multiples of 8 elements;
      tree        NULL or DEVICE [n_rows]: bit j of row i's word lets it see row j of its own sequence
@@ -316,8 +319,9 @@ tactkv_status tactkv_text_read(const tactkv_text_cache* cache, const tactkv_text
    A row that sees nothing gets out = 0, m = -inf, l = 0.  Values at positions that a row does not see
    do not reach it, be they infinities or NaN.  Scores and sums are float32; with bfloat16 q the
    probabilities are rounded to 11 or 8 bits before they multiply V, with float32 q they are not.
-   workspace: tactkv_text_workspace_bytes() with the same numbers, 256-byte aligned; calls that may
-   overlap need workspaces of their own.  Asynchronous on `stream`. */
+   No output may overlap an input or another output.  workspace: tactkv_text_workspace_bytes() with the same
+   numbers, 256-byte aligned; calls that may overlap in time need workspaces of their own.  Asynchronous on
+   `stream`; one kernel, or two where sequences are split. */
 tactkv_status tactkv_text_attention(const tactkv_text_cache* cache, const tactkv_text_batch* batch, int q_heads,
                                     int max_rows, int max_kv_len, const void* q, int64_t q_token_stride,
                                     int64_t q_head_stride, const uint64_t* tree, const float* prior_out,

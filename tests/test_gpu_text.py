@@ -441,6 +441,48 @@ def test_many_sequences():
         check_attention(s, 4, "bf16", prior=True)
 
 
+@pytest.mark.parametrize("fmt,D", [("bf16", 128), ("mxfp8", 256), ("mxfp4", 256), ("mxfp8", 96)])
+def test_offsets_past_32_bits(fmt, D):
+    """A pool of more than 2^32 bytes (2^31 elements at the least), its last pages and first ones in use, against a
+    small pool with the same contents."""
+    heads, page, pages = 8, 64, 5 + 2 ** 32 // (8 * 64 * D * {"bf16": 2, "mxfp8": 1, "mxfp4": 1}[fmt])
+    small = Setup(fmt, heads, D, page, [(4, 333)], seed=1, n_pages=6)
+    row = T.text_cache(fmt, 1, heads, D, page_tokens=page, device=DEV)
+    shape = (pages, *row.k_pages.shape[1:])
+    pools = [torch.empty(shape, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    if fmt != "bf16":
+        pools += [torch.empty((pages, *row.k_scales.shape[1:]), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    big = T.TextCache(fmt, *pools)
+    order = [pages - 1, 0, pages - 3, 2, pages - 2, 1]
+    table = ints([order])
+    k, v = T.text_read(small.cache, small.batch[0], small.batch[1], ints([0, 333]), n_rows=333, dtype=torch.float32)
+    T.text_append(big, k, v, table, small.batch[1], ints([0, 333]), check=True)
+    q = torch.randn((4, 2 * heads, D), device=DEV).bfloat16()
+    want = T.text_attention(q, small.cache, *small.batch, max_rows=4, check=True)
+    got = T.text_attention(q, big, table, *small.batch[1:], max_rows=4, check=True)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    again = T.text_read(big, table, small.batch[1], ints([0, 333]), n_rows=333, dtype=torch.float32, check=True)
+    assert torch.equal(again[0], k) and torch.equal(again[1], v)
+
+
+@pytest.mark.parametrize("layout", ["token", "head", "gaps", "expanded"])
+def test_read_into_strided_outputs(layout):
+    s = Setup("mxfp4", 3, 64, 16, [(5, 40), (2, 7)], seed=8)
+    n = s.n_rows
+    k, v = T.text_read(s.cache, *s.batch, n_rows=n)
+    make = {"token": lambda: torch.empty((n, 3, 64), device=DEV, dtype=torch.bfloat16),
+            "head": lambda: torch.empty((3, n, 64), device=DEV, dtype=torch.bfloat16).transpose(0, 1),
+            "gaps": lambda: torch.empty((n, 3, 2, 64), device=DEV, dtype=torch.bfloat16)[:, :, 0],
+            "expanded": lambda: torch.empty((n, 1, 64), device=DEV, dtype=torch.bfloat16).expand(n, 3, 64)}[layout]
+    out = (make(), make())
+    if layout == "expanded":                              # every head would be written to the same place
+        with pytest.raises(T.TactkvError):
+            T.text_read(s.cache, *s.batch, n_rows=n, out=out)
+        return
+    T.text_read(s.cache, *s.batch, n_rows=n, out=out)
+    assert torch.equal(out[0], k) and torch.equal(out[1], v)
+
+
 # ------------------------------------------------------------------------------------- as it is used ---
 def test_other_stream_and_captured_graph():
     """Calls on a stream of their own, and a captured step replayed on other lengths, pages and rows."""

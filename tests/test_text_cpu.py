@@ -91,6 +91,19 @@ def test_append_and_read_refusals(T, kw, status):
     assert read(T, cache(T), batch(T), **kw) == getattr(T, status)
 
 
+@pytest.mark.parametrize("ts,hs,rows,ok", [
+    (128, 64, 3, True), (128, 62, 3, False), (126, 64, 3, False), (64, 192, 3, True), (64, 190, 3, False), (62, 500, 3, False),
+    (128, 0, 1, False), (2, 64, 1, True), (128, -64, 3, True), (128, -62, 3, False), (256, 128, 3, True), (1 << 62, 1 << 61, 3, True),
+])
+def test_read_refuses_places_that_meet(T, ts, hs, rows, ok):
+    """Two heads of 64.  (Calls that are not refused would launch: the GPU's tests make them.)"""
+    places = {(r, h): r * ts + h * hs for r in range(rows) for h in range(2)}
+    at = sorted(places.values())
+    assert ok == all(b - a >= 64 for a, b in zip(at, at[1:]))          # the parameters themselves
+    if not ok:
+        assert read(T, cache(T), batch(T, n_rows=rows), ts=ts, hs=hs) == T.TACTKV_INVALID_ARG
+
+
 def test_append_values_refusals(T):
     assert append(T, cache(T), batch(T), kv=4096) == T.TACTKV_INVALID_ARG
     assert append(T, cache(T), batch(T), vv=4096) == T.TACTKV_INVALID_ARG
@@ -111,6 +124,12 @@ def test_append_values_refusals(T):
 ])
 def test_attention_refusals(T, kw, status):
     assert attend(T, cache(T), batch(T), **kw) == getattr(T, status)
+
+
+def test_attention_refuses_more_bfloat16_tokens_than_coordinates(T):
+    big = dict(format=0, n_pages=1 << 25, page_tokens=1024, heads=2)
+    assert attend(T, cache(T, **big), batch(T)) == T.TACTKV_UNSUPPORTED_SHAPE
+    assert attend(T, cache(T, **big), batch(T, n_rows=0)) == T.TACTKV_UNSUPPORTED_SHAPE
 
 
 def test_workspace_sizes(T):
