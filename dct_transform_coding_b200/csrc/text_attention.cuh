@@ -17,12 +17,13 @@ namespace text {
 constexpr int kSms = 148;
 constexpr int kMaxParts = 4 * kSms;              // units times parts, where there is more than one part
 constexpr int kLeastPart = 256, kShortPart = 128, kFewParts = 16;   // tokens of a part; see plan()
-constexpr int kWideDim = 128;      // up to this head_dim a unit may have 32 rows (registers for their sums)
+constexpr int kWideDim = 128;      // up to this head_dim a unit may have twice the rows (registers, columns for their sums)
 
 constexpr int kPartRows(int D) { return D <= kWideDim ? 64 : 32; }
 
-// Up to one tile of text_tc.cu's the kernel of text_attention.cu is used: its start is shorter (128 tokens, 4 heads x 128,
-// 8 bits: 7.0 against 9.1 us; from 256 tokens on the other is, 9.6 against 10.1, 4096: 79 against 63).
+// Up to one tile of text_tc.cu's the kernel of text_attention.cu is used: its start is shorter (100 tokens, 4 heads x 128, 8
+// bits: 7.5 against 9.2 us, bfloat16 7.1 against 7.5).  At 256 tokens 8 bits take 9.6 and 10.1 there, bfloat16 9.3 and 8.1,
+// and with more rows or tokens it falls behind (32 sequences x 8 heads x 6001 tokens, 24 rows, 4 bits: 199 against 105).
 constexpr int kOneTile = 128;
 
 // A unit is (sequence, K/V head, tile of tile_rows rows), numbered in that order.

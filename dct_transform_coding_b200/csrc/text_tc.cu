@@ -14,14 +14,14 @@
 // Every wait is bounded; one that expires records TACTKV_TIMEOUT and ends the block's work.
 //
 // The running maximum is lazy: a reference that scores may pass by kSlack before it, the sums and O move, so that O stays in
-// tensor memory (moved with every higher score: 304 against 216 us, 4 sequences x 8 heads x 64 rows, 8111 tokens).
+// tensor memory (moved with every higher score: 258 against 178 us, 4 sequences x 8 heads x 504 rows, 8111 tokens).
 // Coded caches: P is half precision times 2^6 and times its token's V scale relative to the largest so far; with
 // bfloat16 ones P is bfloat16.  Both roundings are half a step of P itself, l is summed in float32 before them.
 //
-// What bounds it, measured with parts of it left out.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, up to 8000 tokens
-// of 16 rows: 122 us, 6.4 TB/s).  Coded ones: the roles' own chains of latencies (in the same sizes 131 us at 8 bits and 127
-// at 4, 3.1 and 1.7 TB/s; decoding and all products left out, still 94 %): a tile of K costs its decoders about 2600
-// cycles, half of it waits and hand-overs, and with 64 rows the softmax 3400.  A block's start and end cost 7 to 12 us.
+// What bounds it.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, 4000 to 8000 tokens, 16 rows: 121 us, 6.5 TB/s).
+// Coded ones: the roles' own chains of latencies (the same sizes: 131 us at 8 bits, 127 at 4, so 3.1 and 1.7 TB/s).  By
+// clock readings in each role a tile of K costs its decoders about 2600 cycles, half of them waits and hand-overs, and
+// with 64 rows a tile costs the softmax about 3400.  A block's start and end cost 7 to 12 us.
 //
 // An infinity or NaN in the V of a drafted token must reach only the rows that see it, so it is taken out of
 // the operand, and its rows get it in plain arithmetic at the end.
@@ -70,14 +70,16 @@ struct Shape {
   // With an odd number of blocks the last product reads a block past V's operand: something must be there.
   static constexpr int kPad = kBlocks % 2 ? kBlock : 0;
   static constexpr int kRest = 1024 + kQ + kPs * kP + kFactors + kTops + kMisc + kPad;
-  // Two blocks on an SM: one's start, end and waits are the other's time.  bfloat16: 20.9 against 23.4 us where a launch is
-  // split into one wave (16 sequences x 4 heads x 128 x 4090 tokens, 7 rows), 122 against 118 in many waves (64 sequences).
-  // Coded: head_dim 64, 64 sequences x 4 heads x 8000 tokens: 112 against 122 us; head_dim 128, 4 bits: 148 against 127.
+  // Two blocks on an SM: one's start, end and waits are the other's time.  bfloat16: 21.1 against 23.4 us where a launch is
+  // split into one wave (16 sequences x 4 heads x 128 x 4090 tokens, 7 rows), 121 against 119 in several (64 sequences x
+  // 8000).  Coded, 64 sequences x 4 heads x 8000 tokens, 16 rows: head_dim 64 109 against 121 us; but 128, 4 bits: 148
+  // against 127.
   static constexpr int kCtas = N <= (kCoded ? 16 : 32) && (!kCoded || D == 64) && kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot <= 113 * 1024 ? 2 : 1;
-  // V operands in turn: two where they leave the raw slots enough (32 sequences x 8 heads, 24 rows: 106 against 113 us)
+  // V operands in turn: two where they leave the raw slots enough (32 sequences x 8 heads, 24 rows: 105 against 111 us)
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
-  // head_dim 256, 130001 tokens: 85 us with 16 warps, 101 with 8; 128, 24 rows: 123 with 16, 106 with 8
+  // head_dim 256, 32 sequences x 4 heads x 8000 tokens: 144 us with 16 warps, 162 with 8; 128, 24 rows: 120 with 16, 105
+  // with 8
   static constexpr int kDecoders = !kCoded ? 0 : (D > 128 ? 16 : 8);
   static constexpr int kThreads = 32 * (4 * kWGs + 2 + kDecoders);
   static constexpr int kFit = ((kCtas == 2 ? 113 : 227) * 1024 - kRest - kOps) / kSlot;
@@ -903,8 +905,8 @@ cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
 }
 template <int FMT>
 cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
-  // The narrowest tile that takes all rows: 64 columns for 16 rows cost 46 us for 39 (8 bits) and 31 for 20 (bfloat16), 8
-  // sequences x 4 heads x 8000 tokens; two tiles of 32 for 64 rows 279 for 191 (64 sequences), since K and V are decoded twice.
+  // The narrowest tile that takes all rows (64 sequences x 4 heads x 8000 tokens, 8 bits): 16 rows in 64 columns take 173
+  // us, in 16 columns 131; 64 rows in two tiles of 32, which decode K and V twice, 277, in one 185.
   const int rows = a.max_rows * (a.q_heads / a.c.heads);
   if (rows <= 16) return launch<FMT, 16>(a, p, st);
   if (rows <= 32 || D > kWideDim) return launch<FMT, 32>(a, p, st);
