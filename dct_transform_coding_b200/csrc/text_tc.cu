@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     }
     if (lane < 2) {
       tc::mbar_init(&bars->s_full[lane], 1);
-      tc::mbar_init(&bars->p_full[lane], 128 * Sh::kWGs);
+      tc::mbar_init(&bars->p_full[lane], 4 * Sh::kWGs);
       tc::mbar_init(&bars->pv_done[lane], 1);
       odd_nodes[lane] = 0;
     }
@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       }
       tc::fence_proxy_async();
       tc::fence_before_sync();
-      tc::mbar_arrive(&bars->p_full[i & 1]);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->p_full[i & 1]);   // (one arrival a warp: a thread's each took turns)
     }
     let_next_start();
     if (ok) ok = wait(&bars->pv_done[(n_tiles - 1) & 1], (n_tiles - 1) / 2 & 1, dead);
