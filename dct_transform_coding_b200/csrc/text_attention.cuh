@@ -22,8 +22,8 @@ constexpr int kWideDim = 128;      // up to this head_dim a unit may have twice 
 constexpr int kPartRows(int D) { return D <= kWideDim ? 64 : 32; }
 
 // Up to one tile of text_tc.cu's the kernel of text_attention.cu is used: its start is shorter (100 tokens, 4 heads x 128, 8
-// bits: 7.5 against 9.2 us, bfloat16 7.1 against 7.5).  At 256 tokens 8 bits take 9.6 and 10.1 there, bfloat16 9.3 and 8.1,
-// and with more rows or tokens it falls behind (32 sequences x 8 heads x 6001 tokens, 24 rows, 4 bits: 199 against 105).
+// bits: 7.3 against 8.7 us, bfloat16 6.8 against 7.1).  At 256 tokens 8 bits take 9.6 and 9.5, bfloat16 9.3 and 7.6,
+// and with more rows or tokens it falls behind (32 sequences x 8 heads x 6001 tokens, 24 rows, 4 bits: 199 against 103).
 constexpr int kOneTile = 128;
 
 // A unit is (sequence, K/V head, tile of tile_rows rows), numbered in that order.
@@ -149,10 +149,10 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 // The split of a launch into at most `blocks` blocks, and each sequence into parts, which have at least kLeastPart tokens:
-// with half of that the sum over more parts costs more than it gains (4000 tokens x 4 heads x 128, tcgen05: bfloat16 11.6
-// against 11.2 us, 8 bits 13.6 against 13.3; head_dim 96 on the other kernel: 17.7 against 13.7).  kShortPart is used where
-// it makes few parts (kFewParts) and no SM gets two: 1000 tokens 9.1 against 9.9 us, 12.1 against 13.2 (350 tokens, 4
-// sequences of 16 rows) and, on the other kernel, 9.7 against 11.8 and 17.3 against 22.8 (float32, head_dim 256).  Sequences
+// with half of that the sum over more parts costs more than it gains (4000 tokens x 4 heads x 128, tcgen05: bfloat16 11.8
+// against 11.2 us, 8 bits 13.5 against 12.6; head_dim 96 on the other kernel: 17.7 against 13.7).  kShortPart is used where
+// it makes few parts (kFewParts) and no SM gets two: 1000 tokens 9.1 against 9.5 us, 8 bits 11.0 against 11.6
+// and, on the other kernel, 9.7 against 11.8 and 17.3 against 22.8 (float32, head_dim 256).  Sequences
 // of up to `whole` tokens are not split.
 inline void plan(const AttnArgs& a, int tile_rows, int blocks, int whole, Parts& p) {
   p.tile_rows = tile_rows;

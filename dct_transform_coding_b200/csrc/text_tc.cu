@@ -14,14 +14,14 @@
 // Every wait is bounded; one that expires records TACTKV_TIMEOUT and ends the block's work.
 //
 // The running maximum is lazy: a reference that scores may pass by kSlack before it, the sums and O move, so that O stays in
-// tensor memory (moved with every higher score: 258 against 178 us, 4 sequences x 8 heads x 504 rows, 8111 tokens).
+// tensor memory (moved with every higher score: 237 against 173 us, 4 sequences x 8 heads x 504 rows, 8111 tokens).
 // Coded caches: P is half precision times 2^6 and times its token's V scale relative to the largest so far; with
 // bfloat16 ones P is bfloat16.  Both roundings are half a step of P itself, l is summed in float32 before them.
 //
-// What bounds it.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, 4000 to 8000 tokens, 16 rows: 121 us, 6.5 TB/s).
-// Coded ones: the roles' own chains of latencies (the same sizes: 131 us at 8 bits, 127 at 4, so 3.1 and 1.7 TB/s).  By
+// What bounds it.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, 4000 to 8000 tokens, 16 rows: 121 to 127 us, 6.2 TB/s).
+// Coded ones: the roles' own chains of latencies (the same sizes: 131 us at 8 bits, 126 at 4, so 3.1 and 1.7 TB/s).  By
 // clock readings in each role a tile of K costs its decoders about 2600 cycles, half of them waits and hand-overs, and
-// with 64 rows a tile costs the softmax about 3400.  A block's start and end cost 7 to 12 us.
+// with 64 rows a tile costs the softmax about 3300.  A block's start and end cost 7 to 12 us.
 //
 // An infinity or NaN in the V of a drafted token must reach only the rows that see it, so it is taken out of
 // the operand, and its rows get it in plain arithmetic at the end.
@@ -70,15 +70,16 @@ struct Shape {
   // With an odd number of blocks the last product reads a block past V's operand: something must be there.
   static constexpr int kPad = kBlocks % 2 ? kBlock : 0;
   static constexpr int kRest = 1024 + kQ + kPs * kP + kFactors + kTops + kMisc + kPad;
-  // Two blocks on an SM: one's start, end and waits are the other's time.  bfloat16: 21.1 against 23.4 us where a launch is
-  // split into one wave (16 sequences x 4 heads x 128 x 4090 tokens, 7 rows), 121 against 119 in several (64 sequences x
-  // 8000).  Coded, 64 sequences x 4 heads x 8000 tokens, 16 rows: head_dim 64 109 against 121 us; but 128, 4 bits: 148
-  // against 127.
-  static constexpr int kCtas = N <= (kCoded ? 16 : 32) && (!kCoded || D == 64) && kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot <= 113 * 1024 ? 2 : 1;
-  // V operands in turn: two where they leave the raw slots enough (32 sequences x 8 heads, 24 rows: 105 against 111 us)
+  // Two blocks on an SM: one's start, end and waits are the other's time.  bfloat16: 21.2 against 23.7 us where a launch is
+  // split into one wave (16 sequences x 4 heads x 128 x 4090 tokens, 7 rows), 127 against 120 in several (64 sequences x
+  // 8000).  Coded, 64 sequences x 4 heads x 8000 tokens, 16 rows: head_dim 64 98 against 121 us; but 128, 4 bits: 136
+  // against 126.
+  static constexpr int kLeast = kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot;   // bytes, with two slots each
+  static constexpr int kCtas = N <= (kCoded ? 16 : 32) && (!kCoded || D == 64) && kLeast <= 113 * 1024 ? 2 : 1;
+  // V operands in turn: two where they leave the raw slots enough (32 sequences x 8 heads, 24 rows: 103 against 109 us)
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
-  // head_dim 256, 32 sequences x 4 heads x 8000 tokens: 144 us with 16 warps, 162 with 8; 128, 24 rows: 120 with 16, 105
+  // head_dim 256, 32 sequences x 4 heads x 8000 tokens: 142 us with 16 warps, 160 with 8; 128, 24 rows: 111 with 16, 103
   // with 8
   static constexpr int kDecoders = !kCoded ? 0 : (D > 128 ? 16 : 8);
   static constexpr int kThreads = 32 * (4 * kWGs + 2 + kDecoders);
@@ -404,63 +405,61 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   } else if (warp == kIssuer) {
     // -------------------------------------------------------------------------------- issuer ---
     // The whole warp goes along, so that descriptors stay in uniform registers; one lane issues.
-    {
-      constexpr uint32_t kIdS = kCoded ? tc::idesc_f16(128, N, false) : tc::idesc_bf16(128, N, false);
-      constexpr uint32_t kIdO = (kCoded ? tc::idesc_f16(128, N, true) : tc::idesc_bf16(128, N, true)) | tc::kIdescBMn;
-      // P is MN-major: a token's N rows are 32, 64 or 128 bytes with the swizzle of that width
-      constexpr uint32_t kSwizzle = N == 16 ? 6 : (N == 32 ? 4 : 2);
-      const uint32_t q_addr = tc::smem_u32(q_op), p_addr = tc::smem_u32(p_op);
-      auto op = [&](int i, int kv) { return kv ? 1 + i % Sh::kVOps : 0; };
-      auto operand = [&](int i, int kv) {
-        return tc::smem_u32(kCoded ? k_op + op(i, kv) * Sh::kOp : slots + slot_of(i, kv, 0) * Sh::kSlot);
-      };
-      auto full = [&](int i, int kv) {
-        return __all_sync(~0u, kCoded ? wait(&bars->op_full[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, dead)
-                                      : wait(&bars->slot_full[slot_of(i, kv, 0)], round_of(i, kv) & 1, dead));
-      };
-      auto release = [&](int i, int kv) {
-        tc::mma_commit(kCoded ? &bars->op_free[op(i, kv)] : &bars->slot_free[slot_of(i, kv, 0)]);
-      };
-      const uint64_t q_desc = tc::smem_desc(q_addr, 16, 1024, 2), p_desc = tc::smem_desc(p_addr, 16, 8 * N * 2, kSwizzle);
-      auto scores = [&](int i) {
-        if (!full(i, 0)) return false;
-        tc::fence_after_sync();
-        const uint64_t k_desc = tc::smem_desc(operand(i, 0), 16, 1024, 2);
-        if (tc::elect_one()) {
+    constexpr uint32_t kIdS = kCoded ? tc::idesc_f16(128, N, false) : tc::idesc_bf16(128, N, false);
+    constexpr uint32_t kIdO = (kCoded ? tc::idesc_f16(128, N, true) : tc::idesc_bf16(128, N, true)) | tc::kIdescBMn;
+    // P is MN-major: a token's N rows are 32, 64 or 128 bytes with the swizzle of that width
+    constexpr uint32_t kSwizzle = N == 16 ? 6 : (N == 32 ? 4 : 2);
+    const uint32_t q_addr = tc::smem_u32(q_op), p_addr = tc::smem_u32(p_op);
+    auto op = [&](int i, int kv) { return kv ? 1 + i % Sh::kVOps : 0; };
+    auto operand = [&](int i, int kv) {
+      return tc::smem_u32(kCoded ? k_op + op(i, kv) * Sh::kOp : slots + slot_of(i, kv, 0) * Sh::kSlot);
+    };
+    auto full = [&](int i, int kv) {
+      return __all_sync(~0u, kCoded ? wait(&bars->op_full[op(i, kv)], (kv ? i / Sh::kVOps : i) & 1, dead)
+                                    : wait(&bars->slot_full[slot_of(i, kv, 0)], round_of(i, kv) & 1, dead));
+    };
+    auto release = [&](int i, int kv) {
+      tc::mma_commit(kCoded ? &bars->op_free[op(i, kv)] : &bars->slot_free[slot_of(i, kv, 0)]);
+    };
+    const uint64_t q_desc = tc::smem_desc(q_addr, 16, 1024, 2), p_desc = tc::smem_desc(p_addr, 16, 8 * N * 2, kSwizzle);
+    auto scores = [&](int i) {
+      if (!full(i, 0)) return false;
+      tc::fence_after_sync();
+      const uint64_t k_desc = tc::smem_desc(operand(i, 0), 16, 1024, 2);
+      if (tc::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)         // addresses in descriptors count 16 bytes
-            tc::mma_bf16(tmem + (i & 1) * N, k_desc + (k / 4 * Sh::kBlock + k % 4 * 32) / 16,
-                         q_desc + (k / 4 * (N * 128) + k % 4 * 32) / 16, kIdS, k > 0);
-          tc::mma_commit(&bars->s_full[i & 1]);
-          release(i, 0);
-        }
-        __syncwarp();
-        return true;
-      };
-      bool ok = scores(0);
-      for (int i = 0; i < n_tiles && ok; ++i) {
-        if (i + 1 < n_tiles) ok = scores(i + 1);
-        if (ok) ok = full(i, 1);
-        if (ok) ok = __all_sync(~0u, wait(&bars->p_full[i & 1], i / 2 & 1, dead));
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint64_t v_desc = tc::smem_desc(operand(i, 1), Sh::kBlock, 1024, 2);
-        if (tc::elect_one()) {
-#pragma unroll
-          for (int g = 0; g < Sh::kGroups; ++g)
-#pragma unroll
-            for (int k = 0; k < TT / 16; ++k)
-              tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16, p_desc + (i % Sh::kPs * Sh::kP + k * (16 * N * 2)) / 16,
-                           kIdO, i > 0 || k > 0);
-          release(i, 1);
-          tc::mma_commit(&bars->pv_done[i & 1]);      // last: whoever sees it knows that every other arrival is in
-        }
-        __syncwarp();
+        for (int k = 0; k < D / 16; ++k)         // addresses in descriptors count 16 bytes
+          tc::mma_bf16(tmem + (i & 1) * N, k_desc + (k / 4 * Sh::kBlock + k % 4 * 32) / 16,
+                       q_desc + (k / 4 * (N * 128) + k % 4 * 32) / 16, kIdS, k > 0);
+        tc::mma_commit(&bars->s_full[i & 1]);
+        release(i, 0);
       }
-      if (!ok) {                                   // products in flight end before tensor memory is released
-        if (tc::elect_one()) tc::mma_commit(&bars->drain);
-        wait(&bars->drain, 0, nullptr);
+      __syncwarp();
+      return true;
+    };
+    bool ok = scores(0);
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      if (i + 1 < n_tiles) ok = scores(i + 1);
+      if (ok) ok = full(i, 1);
+      if (ok) ok = __all_sync(~0u, wait(&bars->p_full[i & 1], i / 2 & 1, dead));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint64_t v_desc = tc::smem_desc(operand(i, 1), Sh::kBlock, 1024, 2);
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int g = 0; g < Sh::kGroups; ++g)
+#pragma unroll
+          for (int k = 0; k < TT / 16; ++k)
+            tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16,
+                         p_desc + (i % Sh::kPs * Sh::kP + k * (16 * N * 2)) / 16, kIdO, i > 0 || k > 0);
+        release(i, 1);
+        tc::mma_commit(&bars->pv_done[i & 1]);   // last: whoever sees it knows that every other arrival is in
       }
+      __syncwarp();
+    }
+    if (!ok) {                                   // products in flight end before tensor memory is released
+      if (tc::elect_one()) tc::mma_commit(&bars->drain);
+      wait(&bars->drain, 0, nullptr);
     }
     __syncwarp();
   } else if (warp < 4 * Sh::kWGs) {
@@ -900,14 +899,14 @@ cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
   }
   CUtensorMap maps[2] = {};
   if (FMT == kBf16 && !(make_map(a, 0, &maps[0]) && make_map(a, 1, &maps[1]))) return cudaErrorInvalidValue;
-  plan(a, N, kSms * Sh::kCtas, 2 * TT, p);   // (two tiles: 8.3 us whole, 9.2 in parts)
+  plan(a, N, kSms * Sh::kCtas, 2 * TT, p);   // (two tiles: 7.6 us whole, 8.5 in parts)
   tc_kernel<FMT, N><<<dim3(p.count, a.c.heads * p.tiles, a.b.n_seqs), Sh::kThreads, Sh::kSmem, st>>>(a, p, maps[0], maps[1]);
   return cudaGetLastError();
 }
 template <int FMT>
 cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
-  // The narrowest tile that takes all rows (64 sequences x 4 heads x 8000 tokens, 8 bits): 16 rows in 64 columns take 173
-  // us, in 16 columns 131; 64 rows in two tiles of 32, which decode K and V twice, 277, in one 185.
+  // The narrowest tile that takes all rows (64 sequences x 4 heads x 8000 tokens, 8 bits): 16 rows in 64 columns take 167
+  // us, in 16 columns 131; 64 rows in two tiles of 32, which decode K and V twice, 272, in one 176.
   const int rows = a.max_rows * (a.q_heads / a.c.heads);
   if (rows <= 16) return launch<FMT, 16>(a, p, st);
   if (rows <= 32 || D > kWideDim) return launch<FMT, 32>(a, p, st);
