@@ -790,12 +790,12 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       return odd != 0;
     };
     const Place mine = place_of(me / 8);
-    bool ok = true;
+    bool ok = true, left = false;
     for (int i = 0; i < n_tiles; ++i) {
       const int slot = slot_of(i, kv, half);
       const int op = kv ? 1 + i % Sh::kVOps : 0, turn = kv ? i / Sh::kVOps : i;
       const int t_half = t0 + i * TT + half * Sh::kPart, held = sp.len - t_half;
-      if (ok) ok = __all_sync(~0u, wait<true>(&bars->slot_full[slot], round_of(i, kv) & 1, dead));
+      ok = __all_sync(~0u, wait<true>(&bars->slot_full[slot], round_of(i, kv) & 1, dead) && !left);
       const uint32_t bad = absent_of[i & 15] >> (half * (Sh::kPart / 16)) & ((1u << Sh::kPart / 16) - 1);
       // One lane to a token: the largest of its scales (the NaN scale aside), and in the scales' place every group's
       // distance to it (31: 2^-25 and less are 0 in half precision; 63: NaN).
@@ -831,8 +831,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (bar_or(6 + 2 * kv + half, kAll, !ok)) break;
       if (kv && me == 0) tc::mbar_arrive(&bars->tops_full[i & 3]);
       if (turn) ok = wait<true>(&bars->op_free[op], (turn - 1) & 1, dead);
-      ok = __all_sync(~0u, ok);
-      if (!ok) continue;                           // a group's warps leave together, at the next tile's barrier
+      left = !__all_sync(~0u, ok);
+      if (left) continue;                          // a group's warps leave together, at the next tile's barrier
       const unsigned char* raw = slots + slot * Sh::kSlot;
       unsigned char* out = k_op + op * Sh::kOp + half * Sh::kPart * 128;
       const bool drafted = kv && t_half + Sh::kPart > before;
