@@ -16,13 +16,12 @@
 // the latency of a warp's steps where there are few.  16 sequences x 4 heads x 128 x 3000 to 6000 tokens, 4 rows, float32
 // queries: bfloat16 cache 66 us, 2.2 TB/s; 8 bits 35 us, 2.1 TB/s; one tile of 100 tokens 7 us.
 //
-// Codes become half precision exactly, scaled by 2^(s - smax) with smax the token's largest scale: in
-// K, 2^smax multiplies the token's score; in V it multiplies the token's probability, relative to the largest
-// smax so far (ref).  A group whose scale is more than 2^15 below its token's largest loses bits that
-// are 2^-24 of the largest.  bfloat16 caches go in as they are.  Queries: bfloat16 ones are exact in
-// either type (half precision: scaled by a power of two for each row; what is 2^-31 of the row's largest element
-// or less loses bits); float32 ones are split into two half-precision or
-// three bfloat16 terms, and so are the probabilities then.
+// A coded value, code * 2^e, is a bfloat16 exactly (what float32 holds below 2^-126 aside), and so it goes into the products:
+// no value needs another's scale, and magnitudes may differ by all that bfloat16 holds, within a token and between tokens,
+// seen or not.  (Half precision relative to the largest scale so far was a product fewer for P and a third fewer for float32
+// queries, but a large V in a token that a row does not see took that row's probabilities below half precision's range.)
+// Queries: bfloat16 ones go in as they are, float32 ones as three bfloat16 terms.  The probabilities are one term for bfloat16
+// caches, two for coded ones, whose values have 4 bits or 2 themselves, and three for float32 queries.
 #include <atomic>
 
 #include "text_attention.cuh"
@@ -61,13 +60,13 @@ struct Shape {
   static constexpr int kStage = kKBytes + kVBytes + 2 * kScaleBytes;
   static constexpr int kStagesFit = 17920 / kStage;
   static constexpr int kStages = kStagesFit < 3 ? 3 : (kStagesFit > 8 ? 8 : kStagesFit);
-  static constexpr int kLimbs = !F32 ? 1 : (kCoded ? 2 : 3);
+  static constexpr int kLimbs = F32 ? 3 : 1, kPLimbs = F32 ? 3 : (kCoded ? 2 : 1);      // bfloat16 terms of q and of P
   static constexpr bool kQInRegs = 2 * NR * kLimbs * (D / 16) <= 32;
   static constexpr int kQBytes = NR * kLimbs * (D / 16) * 32 * 8;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kSum = kWarps * kRows * (D + 4) * 4;       // the warps' sums, over the ring when it is done
   static constexpr int kBody = kRing > kSum ? kRing : kSum;
-  static constexpr int kSmem = kQBytes + kBody + kRows * 8 + kRows * 4 + kWarps * kRows * 8;
+  static constexpr int kSmem = kQBytes + kBody + kRows * 8 + kWarps * kRows * 8;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -96,16 +95,10 @@ __device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)
   }
 }
 
-template <bool HALF>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint2 b) {
-  if constexpr (HALF)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 matrix of 16-bit values across the warp
   uint32_t y;
@@ -116,15 +109,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 matri
 template <int FMT, bool F32, int NR>
 __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, const Parts parts) {
   using Sh = Shape<FMT, F32, NR>;
-  constexpr bool kHalf = Sh::kCoded;
   constexpr int MT = D / 16;                      // 16-column tiles of the output
   constexpr int KS = D / 16;                      // K's steps
   extern __shared__ __align__(16) unsigned char smem[];
   uint2* q_frag = reinterpret_cast<uint2*>(smem);                                 // [limb][step][tile][lane]
   unsigned char* body = smem + Sh::kQBytes;
   unsigned long long* words = reinterpret_cast<unsigned long long*>(body + Sh::kBody);   // [row] what it sees
-  float* row_factors = reinterpret_cast<float*>(words + Sh::kRows);
-  float2* sums = reinterpret_cast<float2*>(row_factors + Sh::kRows);              // [warp][row] (m, l)
+  float2* sums = reinterpret_cast<float2*>(words + Sh::kRows);                    // [warp][row] (m, l)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = lane / 4, c = lane & 3;
   const int G = a.q_heads / a.c.heads;
@@ -197,15 +188,13 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
 
   // ---- the queries' B fragments ----
   // Lane (r, c) of K's step k holds elements idx = 4k .. 4k+3 of its share of row 8n + r: d = (idx / kKElems * 4
-  // + c) * kKElems + idx % kKElems.  For coded caches rows are scaled so that their largest element is in
-  // [2^14, 2^15).
+  // + c) * kKElems + idx % kKElems.
   for (int n = warp; n < NR; n += kWarps) {
     const int row = row0 + 8 * n + r;
     const bool in = row < M;
     const int node = in ? row / G : 0;
     const long long at = (long long)(sp.first + node) * a.q_token + (long long)(head * G + (in ? row % G : 0)) * a.q_head;
     float x[KS][4];
-    uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const int d = (4 * k / Sh::kKElems * 4 + c) * Sh::kKElems + 4 * k % Sh::kKElems;
@@ -218,33 +207,17 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
         x[k][0] = lo.x, x[k][1] = lo.y, x[k][2] = hi.x, x[k][3] = hi.y;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i)
         if (!in) x[k][i] = 0.f;
-        top = max(top, __float_as_uint(x[k][i]) & 0x7FFFFFFFu);
-      }
     }
-    float f = 1.f, back = kToLog2;
-    if constexpr (kHalf) {
-      top = max(top, __shfl_xor_sync(~0u, top, 1));
-      top = max(top, __shfl_xor_sync(~0u, top, 2));
-      const int E = (int)(top >> 23);                         // biased; f = 2^(14 + 127 - E) within float32's range
-      const int e = E == 255 || top == 0 ? 0 : max(-126, min(126, 141 - E));
-      f = __uint_as_float((uint32_t)(127 + e) << 23);
-      back *= __uint_as_float((uint32_t)(127 - e) << 23);
-    }
-    if (c == 0) {
-      row_factors[8 * n + r] = back;
-      words[8 * n + r] = a.tree ? a.tree[sp.first + node] : (node >= 63 ? ~0ull : (2ull << node) - 1);
-    }
+    if (c == 0) words[8 * n + r] = a.tree ? a.tree[sp.first + node] : (node >= 63 ? ~0ull : (2ull << node) - 1);
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[k][i] *= f;
-#pragma unroll
       for (int y = 0; y < Sh::kLimbs; ++y) {
-        const uint2 w = make_uint2(pack2<kHalf>(x[k][0], x[k][1]), pack2<kHalf>(x[k][2], x[k][3]));
+        const uint2 w = make_uint2(pack_bf16x2(x[k][0], x[k][1]), pack_bf16x2(x[k][2], x[k][3]));
         q_frag[((y * KS + k) * NR + n) * 32 + lane] = w;
-        const float2 u = unpack2<kHalf>(w.x), v = unpack2<kHalf>(w.y);
+        const float2 u = unpack_bf16x2(w.x), v = unpack_bf16x2(w.y);
         x[k][0] -= u.x, x[k][1] -= u.y, x[k][2] -= v.x, x[k][3] -= v.y;
       }
     }
@@ -255,19 +228,12 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
 #pragma unroll
     for (int i = 0; i < Sh::kLimbs * KS * NR; ++i) q_reg[i] = q_frag[i * 32 + lane];
   }
-  float row_factor[NR][2];                        // the lane's scores are of rows 8n + 2c and 8n + 2c + 1
-#pragma unroll
-  for (int n = 0; n < NR; ++n)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) row_factor[n][x] = row_factors[8 * n + 2 * c + x];
-
   float o[MT][NR][4] = {};                        // columns r (0, 1) and r + 8 (2, 3) of a tile; rows 2c, 2c + 1
   float m_ref[NR][2], m_true[NR][2], l[NR][2] = {};
 #pragma unroll
   for (int n = 0; n < NR; ++n)
 #pragma unroll
     for (int x = 0; x < 2; ++x) m_ref[n][x] = m_true[n][x] = -INFINITY;
-  uint32_t ref = 0;                               // the largest V scale so far (coded caches)
 
   for (int i = 0; i < steps; ++i) {
     if (i && i % 32 == 0) pages = pages_next, pages_next = page_of(i + 32 + lane);
@@ -286,34 +252,19 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     const int t = (first + i * kWarps) * kStep;
     const int held = sp.len - t;
 
-    // Lane x < 16 finds the largest scale of token x in V, lane 16 + x in K (the NaN scale aside).
-    uint32_t top = 0;
-    if constexpr (Sh::kCoded) {
-      const unsigned char* src = (lane < 16 ? v_scales : k_scales) + (lane & 15) * (D / kGroup);
-#pragma unroll
-      for (int g = 0; g < D / kGroup; ++g) {
-        const uint32_t s = src[g];
-        top = max(top, s == 255u ? 0u : s);
-      }
-      if ((lane & 15) >= held) top = 0;           // what the page holds behind the last token
-    }
-
     // ---- scores: z[n][0, 1]: token r, rows 8n + 2c, + 1;  z[n][2, 3]: token r + 8 ----
     float z[NR][4] = {};
-    uint32_t k_top[2] = {};
     {
       float low[NR][4] = {};                      // the queries' lower terms are summed apart: their rounding stays small
-      uint32_t w[2][Sh::kKVecs][4], f[2][Sh::kKVecs];
+      uint32_t w[2][Sh::kKVecs][4];
+      float f[2][Sh::kKVecs];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (Sh::kCoded) k_top[h] = __shfl_sync(~0u, top, 16 + 8 * h + r);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < Sh::kKVecs; ++j) {
           load_words<Sh::kKVec>(stage + ((h * Sh::kKVecs + j) * 32 + lane) * Sh::kKVec, w[h][j]);
-          if constexpr (Sh::kCoded)
-            f[h][j] = half_factor(k_scales[(8 * h + r) * (D / kGroup) + (j * 4 + c) * Sh::kKElems / kGroup], k_top[h]) * 0x10001u;
+          if constexpr (Sh::kCoded) f[h][j] = scale_value(k_scales[(8 * h + r) * (D / kGroup) + (j * 4 + c) * Sh::kKElems / kGroup]);
         }
-      }
 #pragma unroll
       for (int j = 0; j < Sh::kKVecs; ++j)
 #pragma unroll
@@ -330,7 +281,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
               unpack_e2m1x8(w[h][j][k / 2], u);
               b[h] = u[k % 2 * 2], b[2 + h] = u[k % 2 * 2 + 1];
             }
-            if constexpr (Sh::kCoded) b[h] = mul_half2(b[h], f[h][j]), b[2 + h] = mul_half2(b[2 + h], f[h][j]);
+            if constexpr (Sh::kCoded) b[h] = scaled_bf16x2(b[h], f[h][j], f[h][j]), b[2 + h] = scaled_bf16x2(b[2 + h], f[h][j], f[h][j]);
           }
           const int step = j * (Sh::kKElems / 4) + k;
 #pragma unroll
@@ -342,7 +293,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
               if constexpr (Sh::kQInRegs) q = q_reg[at];
               else q = q_frag[at * 32 + lane];
               // odd steps go into the second sum (without lower terms): two chains of dependent products
-              mma<kHalf>(y || (Sh::kLimbs == 1 && step % 2) ? low[n] : z[n], b, q);
+              mma(y || (Sh::kLimbs == 1 && step % 2) ? low[n] : z[n], b, q);
             }
         }
 #pragma unroll
@@ -350,7 +301,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           z[n][x] += low[n][x];
-          z[n][x] *= (Sh::kCoded ? scale_value(k_top[x / 2]) : 1.f) * row_factor[n][x % 2];
+          z[n][x] *= kToLog2;
         }
     }
     const bool tail = t + kStep > before;
@@ -374,10 +325,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
         m_true[n][x] = fmaxf(m_true[n][x], high);
         over |= high > m_ref[n][x] + kSlack;
       }
-    uint32_t new_ref = ref;
-    if constexpr (Sh::kCoded) new_ref = max(ref, __reduce_max_sync(~0u, lane < 16 ? top : 0u));
-    if (__any_sync(~0u, over) || new_ref != ref) {
-      const float down = Sh::kCoded ? __uint_as_float((uint32_t)max(127 + (int)ref - (int)new_ref, 0) << 23) : 1.f;
+    if (__any_sync(~0u, over)) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -390,21 +338,14 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
           m_ref[n][x] = next;
           l[n][x] *= keep;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) o[mt][n][x] *= keep * down, o[mt][n][2 + x] *= keep * down;
+          for (int mt = 0; mt < MT; ++mt) o[mt][n][x] *= keep, o[mt][n][2 + x] *= keep;
         }
-      ref = new_ref;
     }
 
     // ---- probabilities, and their B fragments: tokens 2c, 2c + 1 (x) and 2c + 8, 2c + 9 (y) of row 8n + r ----
     float p[NR][4];
-    uint2 pb[Sh::kLimbs][NR];
+    uint2 pb[Sh::kPLimbs][NR];
     {
-      float fold[2] = {1.f, 1.f};
-      if constexpr (Sh::kCoded) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          fold[h] = __uint_as_float((uint32_t)max(127 + (int)__shfl_sync(~0u, top, 8 * h + r) - (int)ref, 0) << 23);
-      }
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
 #pragma unroll
@@ -414,15 +355,12 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
         for (int x = 0; x < 2; ++x) l[n][x] += p[n][x] + p[n][2 + x];
         float u[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if constexpr (Sh::kCoded) p[n][x] *= fold[x / 2];
-          u[x] = p[n][x];
-        }
+        for (int x = 0; x < 4; ++x) u[x] = p[n][x];
 #pragma unroll
-        for (int y = 0; y < Sh::kLimbs; ++y) {
-          const uint32_t lo = pack2<kHalf>(u[0], u[1]), hi = pack2<kHalf>(u[2], u[3]);
+        for (int y = 0; y < Sh::kPLimbs; ++y) {
+          const uint32_t lo = pack_bf16x2(u[0], u[1]), hi = pack_bf16x2(u[2], u[3]);
           pb[y][n] = make_uint2(transpose8(lo), transpose8(hi));
-          const float2 v = unpack2<kHalf>(lo), w = unpack2<kHalf>(hi);
+          const float2 v = unpack_bf16x2(lo), w = unpack_bf16x2(hi);
           u[0] -= v.x, u[1] -= v.y, u[2] -= w.x, u[3] -= w.y;
         }
       }
@@ -431,21 +369,19 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     // ---- sums: column r of half tile (j, e) is d = (j * 8 + r) * kVElems + e ----
 #pragma unroll
     for (int j = 0; j < Sh::kVVecs; ++j) {
-      uint32_t w[4][4], f01 = 0, f23 = 0;
+      uint32_t w[4][4];
+      float f[4];                                  // of the tokens, 0 for what the page holds behind the last one
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         load_words<Sh::kVCopy>(stage + Sh::kKBytes + ((n * Sh::kVVecs + j) * 32 + lane) * Sh::kVCopy, w[n]);
         if constexpr (Sh::kVVec < 4) w[n][0] >>= 16 * (r & 1);
       }
       if constexpr (Sh::kCoded) {
-        uint32_t f[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           const int tok = 2 * c + (n & 1) + 8 * (n >> 1);
-          const uint32_t s = v_scales[tok * (D / kGroup) + (j * 8 + r) * Sh::kVElems / kGroup];
-          f[n] = half_factor(tok < held ? s : 0u, __shfl_sync(~0u, top, tok));
+          f[n] = tok < held ? scale_value(v_scales[tok * (D / kGroup) + (j * 8 + r) * Sh::kVElems / kGroup]) : 0.f;
         }
-        f01 = f[0] | f[1] << 16, f23 = f[2] | f[3] << 16;
       }
 #pragma unroll
       for (int e0 = 0; e0 < Sh::kVElems; e0 += 4) {
@@ -474,13 +410,13 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
           }
           if constexpr (Sh::kCoded) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) b[i][side] = mul_half2(b[i][side], side ? f23 : f01);
+            for (int i = 0; i < 4; ++i) b[i][side] = scaled_bf16x2(b[i][side], f[2 * side], f[2 * side + 1]);
           }
         }
         bool odd = false;
         if (tail) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) odd |= odd2<kHalf>(b[i][0]) || odd2<kHalf>(b[i][1]);
+          for (int i = 0; i < 4; ++i) odd |= odd2<false>(b[i][0]) || odd2<false>(b[i][1]);
           odd = __any_sync(~0u, odd);
         }
 #pragma unroll
@@ -489,9 +425,9 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
           if (!odd) {
             const uint32_t av[4] = {b[i][0], b[i + 1][0], b[i][1], b[i + 1][1]};
 #pragma unroll
-            for (int y = 0; y < Sh::kLimbs; ++y)
+            for (int y = 0; y < Sh::kPLimbs; ++y)
 #pragma unroll
-              for (int n = 0; n < NR; ++n) mma<kHalf>(sum[n], av, pb[y][n]);
+              for (int n = 0; n < NR; ++n) mma(sum[n], av, pb[y][n]);
           } else {
             // An infinity or NaN among the drafted tokens' values: only the rows that see it may get it, so
             // the products are summed one by one.  Token 2 cc + x + 8 h of column r is lane (r, cc)'s; its
@@ -501,7 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
               const int h = tok >> 3, node = t + tok - before;
               const uint32_t u = __shfl_sync(~0u, h ? b[i][1] : b[i][0], 4 * r + (tok & 7) / 2),
                              v = __shfl_sync(~0u, h ? b[i + 1][1] : b[i + 1][0], 4 * r + (tok & 7) / 2);
-              const float2 xu = unpack2<kHalf>(u), xv = unpack2<kHalf>(v);
+              const float2 xu = unpack_bf16x2(u), xv = unpack_bf16x2(v);
 #pragma unroll
               for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -524,7 +460,6 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
   // ---- the warps' sums, to the rows' true maxima ----
   __syncthreads();                                 // the ring is done: its place takes the sums
   float* mine = reinterpret_cast<float*>(body) + warp * Sh::kRows * (D + 4);
-  const float unit = Sh::kCoded ? scale_value(ref) : 1.f;
 #pragma unroll
   for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -542,7 +477,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
 #pragma unroll
         for (int e = 0; e < Sh::kVElems; ++e)
           mine[row * (D + 4) + (j * 8 + r) * Sh::kVElems + e] =
-              o[(j * Sh::kVElems + e) / 2][n][e % 2 * 2 + x] * to * unit;
+              o[(j * Sh::kVElems + e) / 2][n][e % 2 * 2 + x] * to;
     }
   __syncthreads();
   for (int i = threadIdx.x; i < Sh::kRows * (D / 4); i += kWarps * 32) {

@@ -77,6 +77,11 @@ __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+// Two half-precision values (codes) times their scales, as bfloat16: exact in its range.
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h, float f, float g) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16x2(v.x * f, v.y * g);
+}
 // 2^(s - top) in half precision (s <= top), NaN for the NaN scale.
 __device__ __forceinline__ uint32_t half_factor(uint32_t s, uint32_t top) {
   const int e = 127 + (int)s - (int)top;

@@ -1,0 +1,124 @@
+"""The text cache's attention where magnitudes differ by more than half precision holds, on the GPU against float64.
+
+Tolerances.  As in test_gpu_text.py a score is off by at most dz = (D / 16 + 4) 2^-23 S, S = sum |q k| / sqrt(D), its
+exponential by 2 dz, and exponentials and float32 sums stay within 2^-16.  The probabilities multiply V as bfloat16 terms,
+each of which leaves at most half a step, 2^-8, of the one before: one term for bfloat16 caches (h_p = 2^-8), two for coded
+ones (2^-16), three for float32 queries (2^-24).  A coded value is a bfloat16 exactly.  So
+  |out error| <= h_out |out| + (h_p + 2 dz + 2^-16) A,   A = sum p |V| / sum p over the tokens that the row sees,
+with no term for values that the row does not see, for other columns', or for tokens of no weight.  (2^-126 stands for what
+float32 drops below its smallest value.)
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import text_plain as P
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from dct_transform_coding_b200 import tactkv as T
+    from test_gpu_text import Setup, ints
+
+DEV = "cuda:0"
+FMTS = ["bf16", "mxfp8", "mxfp4"]
+IO = {"bf16": torch.bfloat16, "f32": torch.float32}
+# (type, head_dim, tokens before the drafted ones, max_kv_len): short calls, head_dims that are not a multiple of 64, and
+# float32 queries take one kernel.  700 tokens of one sequence are split over blocks.
+CALLS = [("bf16", 64, 45, None), ("bf16", 96, 300, None), ("f32", 64, 45, None), ("f32", 128, 45, 2000), ("f32", 256, 700, None)]
+
+
+def strict(s, q, words, got, io, prior=None, seqs=None):
+    """got against the definition, elementwise, with the tolerance above; every finite value of it."""
+    out, m, l = (x.double().cpu().numpy() for x in got)
+    h_out = torch.finfo(IO[io]).eps / 2
+    h_p = 2.0 ** -24 if io == "f32" else (2.0 ** -8 if s.fmt == "bf16" else 2.0 ** -16)
+    q = q.double().cpu().numpy()
+    for i, ((n, t), (K, V)) in enumerate(zip(s.seqs, s.values())):
+        if seqs is not None and i not in seqs:
+            continue
+        lo = s.starts()[i]
+        w = None if words is None else [int(x) & (2 ** 64 - 1) for x in words[lo:lo + n]]
+        pr = None if prior is None else [x[lo:lo + n].double().cpu().numpy() for x in prior]
+        ro, rm, rl, A, S = P.attend(q[lo:lo + n], K, V, P.visible(n, t, w), pr)
+        sl = slice(lo, lo + n)
+        dz = (s.D / 16 + 4) * 2.0 ** -23 * S
+        fin = np.isfinite(rl)
+        assert np.array_equal(np.isfinite(l[sl]), fin)
+        assert (np.abs(m[sl] - rm)[fin] <= (dz + 2.0 ** -22 * np.abs(rm))[fin]).all()
+        assert (np.abs(l[sl] - rl)[fin] <= ((2 * dz + 2.0 ** -16) * rl)[fin]).all()
+        tol = h_out * np.abs(ro) + (h_p + 2 * dz + 2.0 ** -16)[..., None] * A + 2.0 ** -126
+        with np.errstate(invalid="ignore"):
+            bad = ~(np.abs(out[sl] - ro) <= tol) & np.isfinite(ro)
+        assert not bad.any(), (i, np.argwhere(bad)[:4], out[sl][bad][:4], ro[bad][:4], tol[bad][:4])
+        assert np.array_equal(np.isfinite(out[sl]), np.isfinite(ro))
+
+
+def fill(s, k, v):
+    """Every sequence's tokens, in order, written over what the setup wrote."""
+    ends = np.concatenate(([0], np.cumsum([t for _, t in s.seqs]))).tolist()
+    T.text_append(s.cache, k.to(DEV), v.to(DEV), s.batch[0], s.batch[1], ints(ends), check=True)
+
+
+def attend(s, q, words=None, bound=None, **kw):
+    tree = None if words is None else torch.tensor(words, dtype=torch.int64, device=DEV)
+    return T.text_attention(q.to(DEV), s.cache, *s.batch, max_rows=max(n for n, _ in s.seqs), max_kv_len=bound, tree=tree,
+                            check=True, **kw)
+
+
+# ------------------------------------------------------------------- values that a row does not see or weigh ---
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("far", [30, 100])
+@pytest.mark.parametrize("io,D,before,bound", CALLS)
+def test_large_values_of_unseen_drafts_reach_no_row(fmt, io, far, D, before, bound):
+    """Drafted tokens whose V is 2^30 or 2^100 times the others', each seen by its own row alone."""
+    rows, G = 6, 4
+    s = Setup(fmt, 1, D, 32, [(rows, before + rows)], seed=4)
+    t = before + rows
+    k, v = (torch.randn((t, 1, D), generator=s.gen) for _ in range(2))
+    v[before + 2] *= 2.0 ** far
+    v[before + 4] *= 2.0 ** (far - 7)
+    fill(s, k, v)
+    words = [1 << j for j in range(rows)]
+    words[5] |= 1
+    q = torch.randn((rows, G, D), generator=s.gen).to(IO[io])
+    strict(s, q, words, attend(s, q, words, bound), io)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("io,D,before,bound", CALLS)
+def test_large_values_of_no_weight(fmt, io, D, before, bound):
+    """A token that every row sees, with V 2^40 times the others' and a probability below e^-60."""
+    rows, G = 3, 2
+    s = Setup(fmt, 1, D, 16, [(rows, before + rows)], seed=5)
+    t = before + rows
+    k, v = (torch.randn((t, 1, D), generator=s.gen) for _ in range(2))
+    q = torch.randn((rows, G, D), generator=s.gen)
+    q[..., 0] = 4.0
+    k[7, 0] = 0.0
+    k[7, 0, 0] = -30.0 * math.sqrt(D)                     # a score of -120
+    v[7] *= 2.0 ** 40
+    fill(s, k, v)
+    q = q.to(IO[io])
+    strict(s, q, None, attend(s, q, None, bound), io)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("step", [-20, -30, 12])
+@pytest.mark.parametrize("io,D,before,bound", CALLS)
+def test_groups_of_a_token_far_apart(fmt, io, step, D, before, bound):
+    """Each group of 32 columns of V is 2^step times the one before; the queries live in the smallest group of K."""
+    rows, G = 4, 2
+    s = Setup(fmt, 1, D, 16, [(rows, before + rows)], seed=6)
+    t = before + rows
+    k, v = (torch.randn((t, 1, D), generator=s.gen) for _ in range(2))
+    factor = torch.ldexp(torch.ones(D), (torch.arange(D) // 32).clamp(max=3) * step)
+    v *= factor
+    k *= factor
+    small = factor == factor.min()
+    q = torch.where(small, torch.randn((rows, G, D), generator=s.gen) / factor, 0.0)
+    fill(s, k, v)
+    q = q.to(IO[io])
+    strict(s, q, None, attend(s, q, None, bound), io)
