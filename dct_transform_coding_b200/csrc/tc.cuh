@@ -131,12 +131,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn) {
          ((uint32_t)(M >> 4) << 24);
 }
 constexpr uint32_t kIdescBMn = 1u << 16;   // B MN-major
-// The same with half-precision A and B.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn) {
-  return idesc_bf16(M, N, a_mn) & ~((1u << 7) | (1u << 10));
-}
-// D[tmem] (+)= A[smem] * B[smem] (kind::f16, whichever of the two types the descriptor names); issued by a
-// single thread.
+// D[tmem] (+)= A[smem] * B[smem]; issued by a single thread.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"

@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
         bool odd = false;
         if (tail) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) odd |= odd2<false>(b[i][0]) || odd2<false>(b[i][1]);
+          for (int i = 0; i < 4; ++i) odd |= odd2(b[i][0]) || odd2(b[i][1]);
           odd = __any_sync(~0u, odd);
         }
 #pragma unroll

@@ -52,25 +52,6 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 for -inf
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
-template <bool HALF>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (HALF) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    return pack_bf16x2(a, b);
-  }
-}
-template <bool HALF>
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-  if constexpr (HALF) return __half22float2(*reinterpret_cast<const __half2*>(&v));
-  else return unpack_bf16x2(v);
-}
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
 // A pair of E4M3 codes (bits 0-15, or 16-31) as half precision, exactly.
 __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
@@ -82,20 +63,8 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h, float f, float g) 
   const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return pack_bf16x2(v.x * f, v.y * g);
 }
-// 2^(s - top) in half precision (s <= top), NaN for the NaN scale.
-__device__ __forceinline__ uint32_t half_factor(uint32_t s, uint32_t top) {
-  const int e = 127 + (int)s - (int)top;
-  const float f = s == 255u ? NAN : __uint_as_float((uint32_t)max(e, 0) << 23);
-  const __half h = __float2half_rn(f);
-  return *reinterpret_cast<const unsigned short*>(&h);
-}
-
-// Any infinity or NaN among two packed half-precision or bfloat16 values.
-template <bool HALF>
-__device__ __forceinline__ bool odd2(uint32_t v) {
-  constexpr uint32_t e = HALF ? 0x7C00u : 0x7F80u;
-  return (v & e) == e || (v >> 16 & e) == e;
-}
+// Any infinity or NaN among two packed bfloat16 values.
+__device__ __forceinline__ bool odd2(uint32_t v) { return (v & 0x7F80u) == 0x7F80u || (v >> 16 & 0x7F80u) == 0x7F80u; }
 
 constexpr float kLn2 = 0.69314718055994531f;
 

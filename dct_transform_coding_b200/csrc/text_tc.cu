@@ -4,19 +4,21 @@
 // Tiles of 128 tokens are the 128 lanes of tensor memory and a unit's N rows its columns:
 //   S^T[token][row] = K Q^T        A = K  (K-major), B = Q (K-major)
 //   O^T[d][row]    += V^T P^T      A = V^T (the same token rows, MN-major), B = P (K-major)
-// so that a decode step's few rows cost the narrowest product, a thread of the softmax owns one token (its mask, its
-// K and V scales), and bfloat16 pages are operands as TMA delivers them.  Warps by role:
+// so that a decode step's few rows cost the narrowest product, a thread of the softmax owns one token and its mask, and
+// bfloat16 pages are operands as TMA delivers them.  Warps by role:
 //   softmax (4 to 16)  S^T from tensor memory -> P in shared memory; running maxima and sums in registers
 //   producer (1)       copies pages: TMA tiles into operand slots (bfloat16), bulk copies into raw slots (coded)
 //   issuer (1)         all products; the next tile's S^T is issued before this tile's O^T waits for its softmax
-//   decoders (8, 16)   coded caches, in four groups (K or V, half of the tile): each token's largest scale, then the codes
-//                      -> half-precision operands, once for all rows of the unit
+//   decoders (8 to 16) coded caches, in four groups (K or V, half of the tile): codes -> bfloat16 operands, once for all rows
+//                      of the unit
 // Every wait is bounded; one that expires records TACTKV_TIMEOUT and ends the block's work.
 //
 // The running maximum is lazy: a reference that scores may pass by kSlack before it, the sums and O move, so that O stays in
 // tensor memory (moved with every higher score: 237 against 173 us, 4 sequences x 8 heads x 504 rows, 8111 tokens).
-// Coded caches: P is half precision times 2^6 and times its token's V scale relative to the largest so far; with
-// bfloat16 ones P is bfloat16.  Both roundings are half a step of P itself, l is summed in float32 before them.
+// Coded caches: a value, code * 2^e, is a bfloat16 exactly, so no value needs another's scale.  (In half precision relative
+// to the largest scale so far, a large V that a row does not see took the row's probabilities below that type's range.)
+// P is bfloat16: one term for bfloat16 caches, so rounded to 8 bits, two terms, 16 bits, for coded ones, whose products with
+// P's second term take no time that the decoders do not.  l is summed in float32 before the rounding.
 //
 // What bounds it.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, 4000 to 8000 tokens, 16 rows: 121 to 127 us, 6.2 TB/s).
 // Coded ones: the roles' own chains of latencies (the same sizes: 131 us at 8 bits, 126 at 4, so 3.1 and 1.7 TB/s).  By
@@ -62,41 +64,56 @@ struct Shape {
   static constexpr int kParts = kCoded ? 2 : 1, kPart = TT / kParts;            // a slot holds a half or all of K's or V's tile
   static constexpr int kRaw = kPart * kRow, kRawScales = kPart * (D / kGroup);
   static constexpr int kSlot = kCoded ? kRaw + kRawScales : kOp;
-  static constexpr int kQ = kBlocks * N * 128, kP = TT * N * 2;
-  static constexpr int kPs = kCoded && D == 256 && N == 32 ? 1 : 2;             // P's places, in turn (as many as fit)
-  static constexpr int kFactors = kCoded ? 256 : 0;                            // 2^-i, twice in half precision
-  static constexpr int kTops = kCoded ? 8 * TT : 0;                            // [tile % 4][K, V][token]
-  static constexpr int kMisc = 1024 + 24 * N + kWGs * 4 * 8 * R;
+  static constexpr int kQ = kBlocks * N * 128;
+  static constexpr int kPTerms = kCoded ? 2 : 1, kPTerm = TT * N * 2, kP = kPTerms * kPTerm;     // P's bfloat16 terms
+  static constexpr int kMisc = 352 + 12 * N + 144 * kWGs;
   // With an odd number of blocks the last product reads a block past V's operand: something must be there.
   static constexpr int kPad = kBlocks % 2 ? kBlock : 0;
-  static constexpr int kRest = 1024 + kQ + kPs * kP + kFactors + kTops + kMisc + kPad;
+  static constexpr int kFixed = kQ + kMisc + kPad;
   // Two blocks on an SM: one's start, end and waits are the other's time.  bfloat16: 21.2 against 23.7 us where a launch is
   // split into one wave (16 sequences x 4 heads x 128 x 4090 tokens, 7 rows), 127 against 120 in several (64 sequences x
   // 8000).  Coded, 64 sequences x 4 heads x 8000 tokens, 16 rows: head_dim 64 98 against 121 us; but 128, 4 bits: 136
   // against 126.
-  static constexpr int kLeast = kRest + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot;   // bytes, with two slots each
+  static constexpr int kLeast = kFixed + 2 * kP + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot;   // bytes, with two slots each
   static constexpr int kCtas = N <= (kCoded ? 16 : 32) && (!kCoded || D == 64) && kLeast <= 113 * 1024 ? 2 : 1;
   // V operands in turn: two where they leave the raw slots enough (32 sequences x 8 heads, 24 rows: 103 against 109 us)
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
-  // head_dim 256, 32 sequences x 4 heads x 8000 tokens: 142 us with 16 warps, 160 with 8; 128, 24 rows: 111 with 16, 103
-  // with 8
-  static constexpr int kDecoders = !kCoded ? 0 : (D > 128 ? 16 : 8);
+  // head_dim 256, 32 sequences x 4 heads x 8000 tokens: 142 us with 16 warps, 160 with 8; 128, 24 rows: 118 with 16, 114
+  // with 8; 192, of whose three blocks of 64 columns a lane always takes the same one if groups have three warps: 150 with
+  // 12, 179 with 16
+  static constexpr int kDecoders = !kCoded ? 0 : (D == 192 ? 12 : (D > 128 ? 16 : 8));
   static constexpr int kThreads = 32 * (4 * kWGs + 2 + kDecoders);
-  static constexpr int kFit = ((kCtas == 2 ? 113 : 227) * 1024 - kRest - kOps) / kSlot;
+  static constexpr int kMost = (kCtas == 2 ? 113 : 227) * 1024;
+  // P's places, in turn: two where they leave the raw slots' rings as long as one would, or two slots long (head_dim 128, 64
+  // rows, 8 bits: 204 us with two places and rings of one, 189 with one and rings of two)
+  static constexpr int ring(int ps) {
+    const int n = (kMost - kFixed - ps * kP - kOps) / kSlot / 4;
+    return n < 2 ? n : 2;
+  }
+  static constexpr int kPs = !kCoded || ring(2) == ring(1) ? 2 : 1;
+  static constexpr int kFit = (kMost - kFixed - kPs * kP - kOps) / kSlot;
   static constexpr int kSlots = kFit > kMaxSlots ? kMaxSlots : kFit;
-  static constexpr int kSmem = kRest + kOps + kSlots * kSlot;
+  static constexpr int kSmem = kFixed + kPs * kP + kOps + kSlots * kSlot;
   static constexpr int kCols = (2 + kGroups) * N;
   static constexpr int kTmem = kCols <= 32 ? 32 : (kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256));
   static_assert(kSlots >= 2 * kParts && kCols <= 256, "");
   static_assert(N * (D + 4) * 4 <= kOps + (kCoded ? 0 : kSlots * kSlot), "the sums take the operands' place");
+  static_assert(12 * N + kWGs * 4 * 2 * R * 4 <= kP, "and what belongs to the rows' ends P's");
 };
 
 struct Bars {
-  uint64_t slot_full[kMaxSlots], slot_free[kMaxSlots], op_full[3], op_free[3], tops_full[4],
-      s_full[2], p_full[2], pv_done[2], drain;
+  uint64_t slot_full[kMaxSlots], slot_free[kMaxSlots], op_full[3], op_free[3], s_full[2], p_full[2],
+      pv_done[2], drain;
 };
-static_assert(sizeof(Bars) <= 512, "");
+static_assert(sizeof(Bars) <= 304, "");
+// What the warps of a softmax warpgroup tell one another when references move.
+struct Exchange {
+  int most[R];                                     // a row's largest score, as order_of() has it
+  float shift[R];
+  uint32_t moved, unused[3];
+};
+static_assert(sizeof(Exchange) == 144, "");
 
 // False if the phase did not complete within kPolls, or if another wait of the block expired (dead, where given).
 // SLEEP: for waits with time to spare, whose polls would take issue slots from the warps that work.
@@ -137,7 +154,7 @@ __device__ float value_at(const Cache& c, int kv, long long at, int d) {
   uint32_t h[4];
   if constexpr (FMT == kFp8) unpack_e4m3x4(p[d], h[0], h[1]);
   else unpack_e2m1x8(p[d / 2] >> (d % 2 * 4), h);
-  return unpack2<true>(h[0]).x * f;
+  return __low2float(*reinterpret_cast<const __half2*>(&h[0])) * f;
 }
 
 // Two float32 operations in one instruction.
@@ -162,12 +179,16 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
   return y;
 }
-// Not zero if any of 16 half-precision values is an infinity or NaN (its exponent's carry).
-__device__ __forceinline__ uint32_t odd8(const uint32_t (&h)[8]) {
-  uint32_t y = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y |= (h[i] & 0x7C007C00u) + 0x04000400u;
-  return y & 0x80008000u;
+// A number that orders like x, and back.
+__device__ __forceinline__ int order_of(float x) {
+  const int b = __float_as_int(x);
+  return b < 0 ? b ^ 0x7FFFFFFF : b;
+}
+__device__ __forceinline__ float of_order(int b) { return __int_as_float(b < 0 ? b ^ 0x7FFFFFFF : b); }
+// Two half-precision values (codes) times their group's scale, as bfloat16: exact in its range.
+__device__ __forceinline__ uint32_t scaled2(uint32_t h, float2 f) {
+  const float2 v = mul2(__half22float2(*reinterpret_cast<const __half2*>(&h)), f);
+  return pack_bf16x2(v.x, v.y);
 }
 // Sums (or maxima) over the warp of R = 16 values a lane: lane i gets the (i % 16)-th.
 template <int HALF, bool MAX>
@@ -193,27 +214,25 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
               const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<FMT, N>;
   constexpr bool kCoded = Sh::kCoded;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* k_op = smem;                                             // coded: the operands ..
   unsigned char* v_op = k_op + (kCoded ? Sh::kOp : 0);
   unsigned char* q_op = smem + Sh::kOps;
   unsigned char* p_op = q_op + Sh::kQ;
   unsigned char* slots = p_op + Sh::kPs * Sh::kP;                                 // .. and raw slots; bfloat16: operand slots
-  unsigned char* factors = slots + Sh::kSlots * Sh::kSlot + Sh::kPad;
-  unsigned char* tops = factors + Sh::kFactors;
-  unsigned char* misc = tops + Sh::kTops;
+  unsigned char* misc = slots + Sh::kSlots * Sh::kSlot + Sh::kPad;
   Bars* bars = reinterpret_cast<Bars*>(misc);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 512);
-  volatile int* dead = reinterpret_cast<volatile int*>(misc + 516);
-  uint32_t* odd_nodes = reinterpret_cast<uint32_t*>(misc + 520);          // 2 words
-  uint32_t* odd_tile = reinterpret_cast<uint32_t*>(misc + 528);           // decoders met an infinity or NaN in a drafted V
-  uint32_t* absent_of = reinterpret_cast<uint32_t*>(misc + 576);          // [tile % 16] 16-token blocks on bad pages
-  unsigned long long* words = reinterpret_cast<unsigned long long*>(misc + 1024);
-  float2* row_ml = reinterpret_cast<float2*>(words + N);
-  float* row_f = reinterpret_cast<float*>(row_ml + N);                    // a row's factor, its reference's negative
-  float* row_r = row_f + N;
-  float* exchange = row_r + N;                                            // [WG][warp][2 R]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 304);
+  volatile int* dead = reinterpret_cast<volatile int*>(misc + 308);
+  uint32_t* odd_nodes = reinterpret_cast<uint32_t*>(misc + 312);          // 2 words
+  uint32_t* odd_tile = reinterpret_cast<uint32_t*>(misc + 320);           // decoders met an infinity or NaN in a drafted V
+  unsigned char* absent_of = misc + 324;                                  // [tile % 16] 16-token blocks on bad pages, a bit each
+  unsigned long long* words = reinterpret_cast<unsigned long long*>(misc + 352);
+  float* row_r = reinterpret_cast<float*>(words + N);                     // a row's reference's negative
+  Exchange* exchanges = reinterpret_cast<Exchange*>(row_r + N);           // [WG]
+  float2* row_ml = reinterpret_cast<float2*>(p_op);                       // the rows' ends: P is done
+  float* row_f = reinterpret_cast<float*>(row_ml + N);
+  float* ends = row_f + N;                                                // [WG][warp][2 R]
 
   const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x & 31;   // (uniform for the compiler, too)
   const int G = a.q_heads / a.c.heads;
@@ -263,7 +282,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (there && !in) report(a.status);
       bad = __reduce_or_sync(~0u, there && !in ? ((1u << run / 16) - 1) << (lane * run / 16) : 0u);
     }
-    if (lane == 0) absent_of[i & 15] = bad;
+    if (lane == 0) absent_of[i & 15] = (unsigned char)bad;
     at_next = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & (page_tokens - 1));
     __syncwarp();                                  // absent_of before the lanes' arrivals
   };
@@ -306,7 +325,6 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       tc::mbar_init(&bars->slot_full[lane], 1);
       tc::mbar_init(&bars->slot_free[lane], kCoded ? Sh::kDecoders / 4 : 1);
     }
-    if (lane < 4) tc::mbar_init(&bars->tops_full[lane], 2);
     if (lane < 3) {                                // K's operand, V's (one or two)
       tc::mbar_init(&bars->op_full[lane], kCoded ? Sh::kDecoders / 2 : 1);
       tc::mbar_init(&bars->op_free[lane], 1);
@@ -352,33 +370,16 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     for (int x = 0; x < kMine; ++x) {
       const int n = stager + x * kStagers;
       if (n >= N) break;
-      float back = kToLog2;
-      if constexpr (kCoded) {                      // largest element into [2^14, 2^15)
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) top = max(top, max(w[x][i] << 16 & 0x7FFF0000u, w[x][i] & 0x7FFF0000u));
-        top = __reduce_max_sync(~0u, top);
-        const int E8 = (int)(top >> 23), e = E8 == 255 || top == 0 ? 0 : max(-126, min(126, 141 - E8));
-        const float f = __uint_as_float((uint32_t)(127 + e) << 23);
-        back *= __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          const float2 v = unpack_bf16x2(w[x][i]);
-          w[x][i] = pack2<true>(v.x * f, v.y * f);
-        }
-      }
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
         const int d = lane * E + 2 * i;
         *reinterpret_cast<uint32_t*>(q_op + d / 64 * (N * 128) + n * 128 + ((d % 64 / 8) ^ (n & 7)) * 16 + d % 8 * 2) = w[x][i];
       }
       if (lane == 0) {
-        row_f[n] = back, row_r[n] = 0.f;
+        row_r[n] = 0.f;
         words[n] = word[x];
       }
     }
-    if (kCoded && threadIdx.x < 64)
-      reinterpret_cast<uint32_t*>(factors)[threadIdx.x] = half_factor(threadIdx.x == 63 ? 255u : 128u - threadIdx.x, 128u) * 0x10001u;
   }
   tc::fence_proxy_async();
   tc::fence_before_sync();
@@ -405,8 +406,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   } else if (warp == kIssuer) {
     // -------------------------------------------------------------------------------- issuer ---
     // The whole warp goes along, so that descriptors stay in uniform registers; one lane issues.
-    constexpr uint32_t kIdS = kCoded ? tc::idesc_f16(128, N, false) : tc::idesc_bf16(128, N, false);
-    constexpr uint32_t kIdO = (kCoded ? tc::idesc_f16(128, N, true) : tc::idesc_bf16(128, N, true)) | tc::kIdescBMn;
+    constexpr uint32_t kIdS = tc::idesc_bf16(128, N, false), kIdO = tc::idesc_bf16(128, N, true) | tc::kIdescBMn;
     // P is MN-major: a token's N rows are 32, 64 or 128 bytes with the swizzle of that width
     constexpr uint32_t kSwizzle = N == 16 ? 6 : (N == 32 ? 4 : 2);
     const uint32_t q_addr = tc::smem_u32(q_op), p_addr = tc::smem_u32(p_op);
@@ -450,8 +450,10 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         for (int g = 0; g < Sh::kGroups; ++g)
 #pragma unroll
           for (int k = 0; k < TT / 16; ++k)
-            tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16,
-                         p_desc + (i % Sh::kPs * Sh::kP + k * (16 * N * 2)) / 16, kIdO, i > 0 || k > 0);
+#pragma unroll
+            for (int y = 0; y < Sh::kPTerms; ++y)
+              tc::mma_bf16(tmem + (2 + g) * N, v_desc + (2 * g * Sh::kBlock + k * 2048) / 16,
+                           p_desc + (i % Sh::kPs * Sh::kP + y * Sh::kPTerm + k * (16 * N * 2)) / 16, kIdO, i > 0 || k > 0 || y > 0);
         release(i, 1);
         tc::mma_commit(&bars->pv_done[i & 1]);   // last: whoever sees it knows that every other arrival is in
       }
@@ -469,32 +471,25 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     float l[R] = {}, high[R];                      // the thread's tokens' sum, and maximum less the reference
 #pragma unroll
     for (int n = 0; n < R; ++n) high[n] = -INFINITY;
-    uint32_t ref = 0, unset = (1u << R) - 1;       // rows that have seen no score yet (their reference is 0)
+    uint32_t unset = (1u << R) - 1;                // rows that have seen no score yet (their reference is 0)
     bool ok = true;
     for (int i = 0; i < n_tiles; ++i) {
       ok = wait<kCoded>(&bars->s_full[i & 1], i / 2 & 1, dead);
-      if constexpr (kCoded) ok &= wait<true>(&bars->tops_full[i & 3], i / 4 & 1, dead);
       ok = __all_sync(~0u, ok);
       tc::fence_after_sync();
       const int t = t0 + i * TT + tid, node = t - before;
       const uint32_t bad = absent_of[i & 15];
       const bool absent = t >= sp.len || (bad >> (tid / 16) & 1);
       const bool tail = t0 + (i + 1) * TT > before;
-      uint32_t v_top = 0;
-      float k_scale = 1.f;
-      if constexpr (kCoded) {
-        k_scale = scale_value(tops[(i & 3) * 2 * TT + tid]);
-        v_top = tops[((i & 3) * 2 + 1) * TT + tid];
-      }
       float x[R];
       tc::tmem_ld<R>(lanes + (i & 1) * N + rows0, x);
       tc::tmem_ld_wait();
 #pragma unroll
       for (int n = 0; n < R; n += 4) {             // the scores less the references
-        const float4 f = *reinterpret_cast<const float4*>(row_f + rows0 + n), r = *reinterpret_cast<const float4*>(row_r + rows0 + n);
-        const float2 ks = make_float2(k_scale, k_scale);
-        const float2 a = fma2(make_float2(x[n], x[n + 1]), kCoded ? mul2(ks, make_float2(f.x, f.y)) : make_float2(f.x, f.y), make_float2(r.x, r.y));
-        const float2 b = fma2(make_float2(x[n + 2], x[n + 3]), kCoded ? mul2(ks, make_float2(f.z, f.w)) : make_float2(f.z, f.w), make_float2(r.z, r.w));
+        const float4 r = *reinterpret_cast<const float4*>(row_r + rows0 + n);
+        const float2 f = make_float2(kToLog2, kToLog2);
+        const float2 a = fma2(make_float2(x[n], x[n + 1]), f, make_float2(r.x, r.y));
+        const float2 b = fma2(make_float2(x[n + 2], x[n + 3]), f, make_float2(r.z, r.w));
         x[n] = a.x, x[n + 1] = a.y, x[n + 2] = b.x, x[n + 3] = b.y;
       }
       if (tail || bad) {
@@ -507,7 +502,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       float most = -INFINITY;
 #pragma unroll
       for (int n = 0; n < R; ++n) most = fmaxf(most, x[n]);
-      bool move = most > kSlack || v_top > ref || !ok;
+      bool move = most > kSlack || !ok;
       if (unset) {
 #pragma unroll
         for (int n = 0; n < R; ++n) move |= (unset >> n & 1) && x[n] > -INFINITY;
@@ -515,48 +510,37 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (bar_or(bar, 128, move)) {
         if (i) ok &= wait(&bars->pv_done[(i - 1) & 1], (i - 1) / 2 & 1, dead);   // O is whole
         tc::fence_after_sync();
+        Exchange& ex = exchanges[wg];
+        if (tid < R) ex.most[tid] = order_of(-INFINITY);
         if (bar_or(bar, 128, !ok)) break;
-        // move the references: of the rows with such a score, to this tile's largest; of V's scales, to the largest
-        float* mine = exchange + (wg * 4 + (warp & 3)) * 2 * R;
+        // move the references of the rows with such a score to this tile's largest
+        float mine = -INFINITY;                    // lane n: the warp's largest of row n
 #pragma unroll
-        for (int n = 0; n < R; n += 4) {
-          const float4 v = make_float4(warp_max(x[n]), warp_max(x[n + 1]), warp_max(x[n + 2]), warp_max(x[n + 3]));
-          if (lane == 0) *reinterpret_cast<float4*>(mine + n) = v;
+        for (int n = 0; n < R; ++n) {
+          const float v = warp_max(x[n]);
+          if (lane == n) mine = v;
         }
-        const uint32_t top = __reduce_max_sync(~0u, v_top);
-        if (lane == 0) mine[R] = __uint_as_float(top);
+        if (lane < R) atomicMax(&ex.most[lane], order_of(mine));
         bar_sync(bar);
-        float* all = exchange + wg * 4 * 2 * R;
-        uint32_t new_ref = ref;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) new_ref = max(new_ref, __float_as_uint(all[w * 2 * R + R]));
-        float shift = 0.f, scale = 1.f;            // of row rows0 + tid
         if (tid < 32) {
           bool moves = false;
           if (tid < R) {
-            const float by = fmaxf(fmaxf(all[tid], all[2 * R + tid]), fmaxf(all[4 * R + tid], all[6 * R + tid]));
-            const bool first = unset >> tid & 1;
-            moves = by > (first ? -INFINITY : kSlack);
-            if (moves) {
-              shift = by;
-              scale = first ? 0.f : exp2_fast(-by);
-              row_r[rows0 + tid] -= by;
-            }
+            const float by = of_order(ex.most[tid]);
+            moves = by > (unset >> tid & 1 ? -INFINITY : kSlack);
+            ex.shift[tid] = moves ? by : 0.f;
+            if (moves) row_r[rows0 + tid] -= by;
           }
           const uint32_t moved = __ballot_sync(~0u, moves);
-          if (tid == 0) all[4 * R + R + 1] = __uint_as_float(moved);
+          if (tid == 0) ex.moved = moved;
         }
-        bar_sync(bar);                             // the exchanged maxima are read
-        if (tid < R) all[tid] = shift, all[2 * R + tid] = scale;
-        bar_sync(bar);
-        const uint32_t moved = __float_as_uint(all[4 * R + R + 1]);
-        const float down = kCoded ? __uint_as_float((uint32_t)max(127 + (int)ref - (int)new_ref, 0) << 23) : 1.f;
-        ref = new_ref;
+        bar_sync(bar);                             // (the next move's first barriers keep it from what is read here)
+        const uint32_t moved = ex.moved, first = unset & moved;
         unset &= ~moved;
+        auto scale_of = [&](int n) { return first >> n & 1 ? 0.f : exp2_fast(-ex.shift[n]); };
 #pragma unroll
         for (int n = 0; n < R; ++n) {
-          x[n] -= all[n];
-          l[n] *= all[2 * R + n];
+          x[n] -= ex.shift[n];
+          l[n] *= scale_of(n);
           if (moved >> n & 1) high[n] = -INFINITY;  // all before is below this tile's largest
         }
         if (i) {
@@ -569,24 +553,26 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
               tc::tmem_ld<8>(at, v);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int n = 0; n < 8; ++n) v[n] *= all[2 * R + c + n] * down;
+              for (int n = 0; n < 8; ++n) v[n] *= scale_of(c + n);
               tc::tmem_st8(at, v);
             }
           }
           tc::tmem_st_wait();
         }
-        bar_sync(bar);                             // before the exchange's place is written again
       }
-      const float fold = kCoded ? __uint_as_float((uint32_t)max(127 + (int)kBase + (int)v_top - (int)ref, 0) << 23) : 1.f;
-      uint32_t w[R / 2];
+      uint32_t w[Sh::kPTerms][R / 2];
 #pragma unroll
       for (int n = 0; n < R; n += 2) {
-        const float p0 = exp2_fast(x[n]), p1 = exp2_fast(x[n + 1]);
+        float2 p = make_float2(exp2_fast(x[n]), exp2_fast(x[n + 1]));
         high[n] = fmaxf(high[n], x[n]), high[n + 1] = fmaxf(high[n + 1], x[n + 1]);
-        const float2 p = make_float2(p0, p1), sum = add2(make_float2(l[n], l[n + 1]), p);
+        const float2 sum = add2(make_float2(l[n], l[n + 1]), p);
         l[n] = sum.x, l[n + 1] = sum.y;
-        const float2 y = kCoded ? mul2(p, make_float2(fold, fold)) : p;
-        w[n / 2] = pack2<kCoded>(y.x, y.y);
+#pragma unroll
+        for (int y = 0; y < Sh::kPTerms; ++y) {
+          w[y][n / 2] = pack_bf16x2(p.x, p.y);
+          const float2 u = unpack_bf16x2(w[y][n / 2]);
+          p = add2(p, make_float2(-u.x, -u.y));
+        }
       }
       if (i >= Sh::kPs) ok = wait(&bars->pv_done[(i - Sh::kPs) & 1], (i - Sh::kPs) / 2 & 1, dead);   // P's place is free
       ok = __all_sync(~0u, ok);
@@ -594,8 +580,11 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       unsigned char* p_at = p_op + i % Sh::kPs * Sh::kP + tid * (N * 2);
       const int turn = N == 16 ? tid >> 2 & 1 : (N == 32 ? tid >> 1 & 3 : tid & 7);
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
-        *reinterpret_cast<uint4*>(p_at + (((rows0 / 8 + y) ^ turn) << 4)) = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+      for (int z = 0; z < Sh::kPTerms; ++z)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          *reinterpret_cast<uint4*>(p_at + z * Sh::kPTerm + (((rows0 / 8 + y) ^ turn) << 4)) =
+              make_uint4(w[z][4 * y], w[z][4 * y + 1], w[z][4 * y + 2], w[z][4 * y + 3]);
       // Behind the last token V's operand holds whatever the page holds (decoders write zeros there), and a
       // drafted token's infinities and NaN are for some rows only: zeros take their place.
       if (wg == 0 && (tail || (bad && !kCoded))) {
@@ -619,12 +608,12 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
           const int tok = from + y / (D / 8), c = y % (D / 8);
           uint4* at = reinterpret_cast<uint4*>(v + c / 8 * Sh::kBlock + tok * 128 + c % 8 * 16);
           uint32_t u[4] = {at->x, at->y, at->z, at->w};
-          if ((bad >> (tok / 16) & 1) || !(odd2<kCoded>(u[0]) || odd2<kCoded>(u[1]) || odd2<kCoded>(u[2]) || odd2<kCoded>(u[3])))
+          if ((bad >> (tok / 16) & 1) || !(odd2(u[0]) || odd2(u[1]) || odd2(u[2]) || odd2(u[3])))
             continue;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (odd2<kCoded>(u[e] & 0xFFFFu)) u[e] &= 0xFFFF0000u;
-            if (odd2<kCoded>(u[e] & 0xFFFF0000u)) u[e] &= 0xFFFFu;
+            if (odd2(u[e] & 0xFFFFu)) u[e] &= 0xFFFF0000u;
+            if (odd2(u[e] & 0xFFFF0000u)) u[e] &= 0xFFFFu;
           }
           *at = make_uint4(u[0], u[1], u[2], u[3]);
           const int j = base + tok - before;
@@ -646,20 +635,20 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       const float above = reduce_rows<true>(high);
       const float total = reduce_rows<false>(l);
       if (lane < R) {
-        exchange[(wg * 4 + (warp & 3)) * 2 * R + lane] = above;
-        exchange[(wg * 4 + (warp & 3)) * 2 * R + R + lane] = total;
+        ends[(wg * 4 + (warp & 3)) * 2 * R + lane] = above;
+        ends[(wg * 4 + (warp & 3)) * 2 * R + R + lane] = total;
       }
       bar_sync(bar);
       if (tid < R) {
         float m = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          m = fmaxf(m, exchange[(wg * 4 + w) * 2 * R + tid]);
-          sum += exchange[(wg * 4 + w) * 2 * R + R + tid];
+          m = fmaxf(m, ends[(wg * 4 + w) * 2 * R + tid]);
+          sum += ends[(wg * 4 + w) * 2 * R + R + tid];
         }
         const float to = m == -INFINITY ? 0.f : exp2f(-m);
         row_ml[rows0 + tid] = make_float2(m == -INFINITY ? m : m - row_r[rows0 + tid], sum * to);
-        row_f[rows0 + tid] = to * (kCoded ? scale_value(ref) * 0.015625f : 1.f);   // of the row's sums
+        row_f[rows0 + tid] = to;                   // of the row's sums
       }
       bar_sync(bar);
       float* sums = reinterpret_cast<float*>(kCoded ? smem : slots);
@@ -680,7 +669,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         if (t < t0 || t >= t0 + n_tiles * TT) continue;
         const int page = __ldg(a.b.table + (long long)seq * a.b.max_pages + (t >> a.c.page_log2));
         const long long at = (((long long)page * a.c.heads + head) << a.c.page_log2) + (t & ((1 << a.c.page_log2) - 1));
-        float* p_row = exchange + wg * 4 * 2 * R;
+        float* p_row = ends + wg * 4 * 2 * R;
         bar_sync(bar);
         if (tid < R) {
           const int row = row0 + rows0 + tid;
@@ -731,13 +720,11 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     // Four groups: for K and for V, for a tile's first 64 tokens and for the rest.
     constexpr int kAll = 8 * Sh::kDecoders, kGroupsRow = D / kGroup;
     constexpr int kItems = Sh::kPart / 4 * Sh::kBlocks;                    // of eight lanes, in a slot
-    constexpr int kPasses = (kItems + kAll / 8 - 1) / (kAll / 8);
+    constexpr int kPasses = kItems / (kAll / 8);
     const int of = threadIdx.x - 32 * (kIssuer + 1), kv = of / kAll / 2, half = of / kAll % 2, me = of % kAll;
-    // Where D is 64, 128 or 256 a lane's block, group and token modulo 8 are the same in every pass, and with them
-    // all of its offsets but for constants.
-    constexpr bool kSteady = kAll / 8 % Sh::kBlocks == 0;
+    // A lane's block, group and token modulo 8 are the same in every pass, and with them all of its offsets but for constants.
     constexpr int kStep = kAll / 8 / Sh::kBlocks * 4;                      // tokens from pass to pass
-    static_assert(!kSteady || (kStep % 8 == 0 && kItems % (kAll / 8) == 0), "");
+    static_assert(kAll / 8 % Sh::kBlocks == 0 && kStep % 8 == 0 && kItems % (kAll / 8) == 0, "");
     struct Place {
       int tok, g, raw, scale, out, chunk[4];
     };
@@ -753,97 +740,55 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       for (int y = 0; y < 4; ++y) p.chunk[y] = ((sub * 4 + (FMT == kFp8 ? y ^ (p.tok & 1) * 2 : y)) ^ (p.tok & 7)) * 16;
       return p;
     };
-    // One group: its codes, scaled, to the operand.  Returns whether it may hold an infinity or NaN.
+    // One group: its codes, scaled, to the operand.  Returns whether it holds an infinity or NaN, if asked to look.
     auto decode = [&](const unsigned char* raw, unsigned char* out, const Place& p, int pass, bool absent, bool look) {
-      const uint32_t f = reinterpret_cast<const uint32_t*>(factors)[raw[p.scale + pass * kStep * kGroupsRow]];
+      const float s = absent ? 0.f : scale_value(raw[p.scale + pass * kStep * kGroupsRow]);
+      const float2 f = make_float2(s, s);
       const unsigned char* from = raw + p.raw + pass * kStep * Sh::kRow;
       unsigned char* to = out + p.out + pass * kStep * 128;
-      uint32_t odd = 0;
-      if constexpr (FMT == kFp8) {
+      bool odd = false;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {              // the half that the lane takes first alternates with its token
-          uint4 w = *reinterpret_cast<const uint4*>(from + ((y ^ (p.tok & 1)) * 16));
-          if (absent) w = make_uint4(0, 0, 0, 0);
-          uint32_t h[8];
-          unpack_e4m3x4(w.x, h[0], h[1]);
-          unpack_e4m3x4(w.y, h[2], h[3]);
-          unpack_e4m3x4(w.z, h[4], h[5]);
-          unpack_e4m3x4(w.w, h[6], h[7]);
-#pragma unroll
-          for (int z = 0; z < 8; ++z) h[z] = mul_half2(h[z], f);
-          *reinterpret_cast<uint4*>(to + p.chunk[2 * y]) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(to + p.chunk[2 * y + 1]) = make_uint4(h[4], h[5], h[6], h[7]);
-          if (look) odd |= odd8(h);
-        }
-      } else {
-        uint4 w = *reinterpret_cast<const uint4*>(from);
+      for (int y = 0; y < (FMT == kFp8 ? 2 : 1); ++y) {   // the half that the lane takes first alternates with its token
+        uint4 w = *reinterpret_cast<const uint4*>(from + (FMT == kFp8 ? (y ^ (p.tok & 1)) * 16 : 0));
         if (absent) w = make_uint4(0, 0, 0, 0);
         const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int c = 0; c < (FMT == kFp8 ? 2 : 4); ++c) {
           uint32_t h[4];
-          unpack_e2m1x8(in[y], h);
-          *reinterpret_cast<uint4*>(to + p.chunk[y]) = make_uint4(mul_half2(h[0], f), mul_half2(h[1], f), mul_half2(h[2], f), mul_half2(h[3], f));
+          if constexpr (FMT == kFp8) {
+            unpack_e4m3x4(in[2 * c], h[0], h[1]);
+            unpack_e4m3x4(in[2 * c + 1], h[2], h[3]);
+          } else {
+            unpack_e2m1x8(in[c], h);
+          }
+#pragma unroll
+          for (int z = 0; z < 4; ++z) h[z] = scaled2(h[z], f);
+          *reinterpret_cast<uint4*>(to + p.chunk[FMT == kFp8 ? 2 * y + c : c]) = make_uint4(h[0], h[1], h[2], h[3]);
+          if (look) odd |= odd2(h[0]) || odd2(h[1]) || odd2(h[2]) || odd2(h[3]);
         }
-        odd = (f & 0x7C00u) == 0x7C00u;            // E2M1 itself has no infinity or NaN
       }
-      return odd != 0;
+      return odd;
     };
     const Place mine = place_of(me / 8);
-    bool ok = true, left = false;
+    bool ok = true;
     for (int i = 0; i < n_tiles; ++i) {
       const int slot = slot_of(i, kv, half);
       const int op = kv ? 1 + i % Sh::kVOps : 0, turn = kv ? i / Sh::kVOps : i;
       const int t_half = t0 + i * TT + half * Sh::kPart, held = sp.len - t_half;
-      ok = __all_sync(~0u, wait<true>(&bars->slot_full[slot], round_of(i, kv) & 1, dead) && !left);
+      ok = wait<true>(&bars->slot_full[slot], round_of(i, kv) & 1, dead);
+      if (turn) ok = ok && wait<true>(&bars->op_free[op], (turn - 1) & 1, dead);
+      if (!__all_sync(~0u, ok)) break;
       const uint32_t bad = absent_of[i & 15] >> (half * (Sh::kPart / 16)) & ((1u << Sh::kPart / 16) - 1);
-      // One lane to a token: the largest of its scales (the NaN scale aside), and in the scales' place every group's
-      // distance to it (31: 2^-25 and less are 0 in half precision; 63: NaN).
-      if (ok && me < Sh::kPart) {
-        const bool absent = me >= held || (bad >> (me / 16) & 1);
-        unsigned char* sc = slots + slot * Sh::kSlot + Sh::kRaw + me * kGroupsRow;
-        uint32_t b[kGroupsRow], top = 0;
-        if constexpr (kGroupsRow % 4 == 0) {
-#pragma unroll
-          for (int g = 0; g < kGroupsRow; g += 4) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + g);
-            b[g] = w & 255u, b[g + 1] = w >> 8 & 255u, b[g + 2] = w >> 16 & 255u, b[g + 3] = w >> 24;
-          }
-        } else {
-#pragma unroll
-          for (int g = 0; g < kGroupsRow; ++g) b[g] = sc[g];
-        }
-#pragma unroll
-        for (int g = 0; g < kGroupsRow; ++g) top = max(top, b[g] == 255u ? 0u : b[g]);
-        if (absent) top = 0;
-        tops[((i & 3) * 2 + kv) * TT + half * Sh::kPart + me] = (unsigned char)top;
-#pragma unroll
-        for (int g = 0; g < kGroupsRow; ++g) b[g] = absent ? 0u : (b[g] == 255u ? 63u : min(top - min(b[g], top), 31u));
-        if constexpr (kGroupsRow % 4 == 0) {
-#pragma unroll
-          for (int g = 0; g < kGroupsRow; g += 4)
-            *reinterpret_cast<uint32_t*>(sc + g) = b[g] | b[g + 1] << 8 | b[g + 2] << 16 | b[g + 3] << 24;
-        } else {
-#pragma unroll
-          for (int g = 0; g < kGroupsRow; ++g) sc[g] = (unsigned char)b[g];
-        }
-      }
-      if (bar_or(6 + 2 * kv + half, kAll, !ok)) break;
-      if (kv && me == 0) tc::mbar_arrive(&bars->tops_full[i & 3]);
-      if (turn) ok = wait<true>(&bars->op_free[op], (turn - 1) & 1, dead);
-      left = !__all_sync(~0u, ok);
-      if (left) continue;                          // a group's warps leave together, at the next tile's barrier
       const unsigned char* raw = slots + slot * Sh::kSlot;
       unsigned char* out = k_op + op * Sh::kOp + half * Sh::kPart * 128;
       const bool drafted = kv && t_half + Sh::kPart > before;
-      if (kSteady && held >= Sh::kPart && !bad && !drafted) {
+      if (held >= Sh::kPart && !bad && !drafted) {
 #pragma unroll
         for (int pass = 0; pass < kPasses; ++pass) decode(raw, out, mine, pass, false, false);
       } else {
         bool odd = false;
         for (int pass = 0; pass < kPasses; ++pass) {
           const int item = me / 8 + pass * (kAll / 8);
-          if (item >= kItems) break;
           const Place p = place_of(item);
           const bool absent = p.tok >= held || (bad >> (p.tok / 16) & 1), look = drafted && t_half + p.tok >= before;
           odd |= decode(raw, out, p, 0, absent, look) && look && !absent;

@@ -26,8 +26,9 @@ DEV = "cuda:0"
 FMTS = ["bf16", "mxfp8", "mxfp4"]
 IO = {"bf16": torch.bfloat16, "f32": torch.float32}
 # (type, head_dim, tokens before the drafted ones, max_kv_len): short calls, head_dims that are not a multiple of 64, and
-# float32 queries take one kernel.  700 tokens of one sequence are split over blocks.
-CALLS = [("bf16", 64, 45, None), ("bf16", 96, 300, None), ("f32", 64, 45, None), ("f32", 128, 45, 2000), ("f32", 256, 700, None)]
+# float32 queries take one kernel, the last four the other.  700 tokens of one sequence are split over blocks.
+CALLS = [("bf16", 64, 45, None), ("bf16", 96, 300, None), ("f32", 64, 45, None), ("f32", 128, 45, 2000), ("f32", 256, 700, None),
+         ("bf16", 64, 45, 2000), ("bf16", 128, 45, 2000), ("bf16", 256, 700, None), ("bf16", 192, 250, None)]
 
 
 def strict(s, q, words, got, io, prior=None, seqs=None):
