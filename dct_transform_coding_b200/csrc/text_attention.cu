@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
         l[n][x] += __shfl_xor_sync(~0u, l[n][x], y);
       }
       const int row = 8 * n + 2 * c + x;
-      const float to = m_true[n][x] == -INFINITY ? 0.f : exp2f(m_ref[n][x] - m_true[n][x] - kBase);
-      if (r == 0) sums[warp * Sh::kRows + row] = make_float2(m_true[n][x], l[n][x] * (l[n][x] == l[n][x] ? to : 1.f));
+      const float to = m_true[n][x] == -INFINITY ? 0.f : exp2f(m_ref[n][x] - m_true[n][x]);
+      if (r == 0) sums[warp * Sh::kRows + row] = make_float2(m_true[n][x], l[n][x] * (l[n][x] == l[n][x] ? to * kUnbase : 1.f));
 #pragma unroll
       for (int j = 0; j < Sh::kVVecs; ++j)
 #pragma unroll

@@ -32,12 +32,16 @@ struct Parts {
   int tiles;           // for max_rows * G rows
   int tokens;          // per part, a multiple of 128
   int count;           // parts of the longest sequence
-  float* o;            // [count][unit][tile_rows][D] sums of exp2(z - m) V
+  float* o;            // [count][unit][tile_rows][D] sums of exp2(z - m) V, times 2^kBase
   float2* ml;          // [count][unit][tile_rows] m (log2), l
 };
 
-constexpr float kBase = 6.f;         // probabilities are held times 2^6 ..
-constexpr float kSlack = 8.f;        // .. relative to a maximum that may be 8 below the true one: at most 2^14
+// Probabilities are held times 2^kBase until a row's end, relative to a maximum that may be kSlack below the true one, so as
+// at most 2^-8: float32 sums of any 256 tokens stay finite for all that bfloat16 holds, of 2^16 tokens for |V| up to 2^120,
+// of 2^30 up to 2^106.  (At 2^6 one dominant token's V of 2^114 reached infinity.)  The price is at the other end: products
+// below 2^-126 lose bits, so those of |V| below 2^-102 and p below 2^-8.
+constexpr float kBase = -16.f, kSlack = 8.f;
+constexpr float kUnbase = 65536.f;   // 2^-kBase
 
 constexpr double root(double x) {                // by Newton's iteration, at compile time
   double y = x;
@@ -68,7 +72,7 @@ __device__ __forceinline__ bool odd2(uint32_t v) { return (v & 0x7F80u) == 0x7F8
 
 constexpr float kLn2 = 0.69314718055994531f;
 
-// A row's end: out = a * (the text tokens' sum) + b * prior_out.
+// A row's end: out = a * (the text tokens' sum, times 2^kBase) + b * prior_out.
 struct RowEnd {
   float a, b;
 };
@@ -84,7 +88,7 @@ __device__ __forceinline__ RowEnd end_row(const AttnArgs& a, long long at, float
     m = l == l ? top : l;
   }
   if (write) a.m[at] = m, a.l[at] = l;
-  return l == 0.f ? RowEnd{0.f, 0.f} : RowEnd{x / l, y == 0.f ? 0.f : y / l};   // b = 0 without a prior, l a NaN or not
+  return l == 0.f ? RowEnd{0.f, 0.f} : RowEnd{x / l * kUnbase, y == 0.f ? 0.f : y / l};   // b = 0 without a prior, l a NaN or not
 }
 // Columns d .. d+3 of a row with the sum o.
 template <bool F32>

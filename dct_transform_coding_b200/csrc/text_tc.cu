@@ -567,6 +567,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         high[n] = fmaxf(high[n], x[n]), high[n + 1] = fmaxf(high[n + 1], x[n + 1]);
         const float2 sum = add2(make_float2(l[n], l[n + 1]), p);
         l[n] = sum.x, l[n + 1] = sum.y;
+        // (2^kBase as part of the references would take a bit of 2^-20 from the scores)
+        p = mul2(p, make_float2(1.f / kUnbase, 1.f / kUnbase));
 #pragma unroll
         for (int y = 0; y < Sh::kPTerms; ++y) {
           w[y][n / 2] = pack_bf16x2(p.x, p.y);
@@ -648,7 +650,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         }
         const float to = m == -INFINITY ? 0.f : exp2f(-m);
         row_ml[rows0 + tid] = make_float2(m == -INFINITY ? m : m - row_r[rows0 + tid], sum * to);
-        row_f[rows0 + tid] = to;                   // of the row's sums
+        row_f[rows0 + tid] = to;                   // of the row's sums, which stay times 2^kBase
       }
       bar_sync(bar);
       float* sums = reinterpret_cast<float*>(kCoded ? smem : slots);

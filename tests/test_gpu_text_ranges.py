@@ -123,3 +123,23 @@ def test_groups_of_a_token_far_apart(fmt, io, step, D, before, bound):
     fill(s, k, v)
     q = q.to(IO[io])
     strict(s, q, None, attend(s, q, None, bound), io)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("io,D,before,bound", CALLS)
+def test_values_near_the_largest(fmt, io, D, before, bound):
+    """V of one sign up to 2.5e38, whose sums pass float32's range, and a late token of most of the weight whose score is
+    not far enough above the others' for the running maximum to follow it at once."""
+    rows, G = 3, 2
+    s = Setup(fmt, 1, D, 16, [(rows, before + rows)], seed=7)
+    t = before + rows
+    k, v = (torch.randn((t, 1, D), generator=s.gen) for _ in range(2))
+    v = 2.5e38 * (0.5 + 0.5 * torch.rand((t, 1, D), generator=s.gen))
+    q = torch.randn((rows, G, D), generator=s.gen)
+    q[..., 0] = 4.0
+    k[..., 0] = 0.0
+    k[t - rows - 1] = 0.0
+    k[t - rows - 1, 0, 0] = 2.0 * math.sqrt(D)            # a score of 8 beside others of about 1
+    fill(s, k, v)
+    q = q.to(IO[io])
+    strict(s, q, None, attend(s, q, None, bound), io)
