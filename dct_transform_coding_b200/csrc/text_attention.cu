@@ -215,10 +215,12 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     for (int k = 0; k < KS; ++k) {
 #pragma unroll
       for (int y = 0; y < Sh::kLimbs; ++y) {
-        const uint2 w = make_uint2(pack_bf16x2(x[k][0], x[k][1]), pack_bf16x2(x[k][2], x[k][3]));
+        const uint2 w = make_uint2(pack_bf16x2_rz(x[k][0], x[k][1]), pack_bf16x2_rz(x[k][2], x[k][3]));
         q_frag[((y * KS + k) * NR + n) * 32 + lane] = w;
         const float2 u = unpack_bf16x2(w.x), v = unpack_bf16x2(w.y);
-        x[k][0] -= u.x, x[k][1] -= u.y, x[k][2] -= v.x, x[k][3] -= v.y;
+        const float held[4] = {u.x, u.y, v.x, v.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[k][i] = x[k][i] == held[i] ? 0.f : x[k][i] - held[i];   // nothing is left of an infinity
       }
     }
   }

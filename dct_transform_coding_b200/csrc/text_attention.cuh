@@ -56,6 +56,12 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 for -inf
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// Rounded towards zero: never an infinity, and three such terms hold every bit of a float32.
+__device__ __forceinline__ uint32_t pack_bf16x2_rz(float a, float b) {
+  uint32_t y;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;\n" : "=r"(y) : "f"(b), "f"(a));
+  return y;
+}
 // A pair of E4M3 codes (bits 0-15, or 16-31) as half precision, exactly.
 __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"

@@ -143,3 +143,18 @@ def test_values_near_the_largest(fmt, io, D, before, bound):
     fill(s, k, v)
     q = q.to(IO[io])
     strict(s, q, None, attend(s, q, None, bound), io)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,before,bound", [(64, 45, None), (128, 300, 2000)])
+def test_queries_near_the_largest(fmt, D, before, bound):
+    """float32 queries above bfloat16's largest value, against a group of K near its smallest."""
+    rows, G = 3, 2
+    s = Setup(fmt, 1, D, 16, [(rows, before + rows)], seed=8)
+    k, v = (torch.randn((before + rows, 1, D), generator=s.gen) for _ in range(2))
+    k[..., :32] *= 1e-37
+    fill(s, k, v)
+    q = torch.randn((rows, G, D), generator=s.gen)
+    q[..., 3] = 3.4e38
+    q[0, 1, 9] = -3.4e38
+    strict(s, q, None, attend(s, q, None, bound), "f32")
