@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float high = fmaxf(z[n][x], z[n][2 + x]);
-        m_true[n][x] = fmaxf(m_true[n][x], high);
+        m_true[n][x] = max_nan(m_true[n][x], max_nan(z[n][x], z[n][2 + x]));
         over |= high > m_ref[n][x] + kSlack;
       }
     if (__any_sync(~0u, over)) {
@@ -468,12 +468,12 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     for (int x = 0; x < 2; ++x) {
 #pragma unroll
       for (int y = 4; y <= 16; y *= 2) {
-        m_true[n][x] = fmaxf(m_true[n][x], __shfl_xor_sync(~0u, m_true[n][x], y));
+        m_true[n][x] = max_nan(m_true[n][x], __shfl_xor_sync(~0u, m_true[n][x], y));
         l[n][x] += __shfl_xor_sync(~0u, l[n][x], y);
       }
       const int row = 8 * n + 2 * c + x;
       const float to = m_true[n][x] == -INFINITY ? 0.f : exp2f(m_ref[n][x] - m_true[n][x]);
-      if (r == 0) sums[warp * Sh::kRows + row] = make_float2(m_true[n][x], l[n][x] * (l[n][x] == l[n][x] ? to * kUnbase : 1.f));
+      if (r == 0) sums[warp * Sh::kRows + row] = make_float2(m_true[n][x], l[n][x] * (to * kUnbase));
 #pragma unroll
       for (int j = 0; j < Sh::kVVecs; ++j)
 #pragma unroll
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kWarps * 32) parts_kernel(const AttnArgs a, co
     if (row >= M) break;
     float m = -INFINITY, lsum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sums[w * Sh::kRows + lr].x);
+    for (int w = 0; w < kWarps; ++w) m = max_nan(m, sums[w * Sh::kRows + lr].x);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {

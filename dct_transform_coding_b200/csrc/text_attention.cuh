@@ -56,6 +56,11 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 for -inf
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 // Rounded towards zero: never an infinity, and three such terms hold every bit of a float32.
 __device__ __forceinline__ uint32_t pack_bf16x2_rz(float a, float b) {
   uint32_t y;
@@ -83,15 +88,15 @@ struct RowEnd {
   float a, b;
 };
 // Of (row, head) number `at`, from the text tokens' maximum m2 (log2) and l, merged with the prior; write: m and l, too.
-// A row that sees nothing has l = 0: out = 0, m = -inf.
+// A row that sees nothing has l = 0: out = 0, m = -inf.  One with a score of +inf or NaN has that as m2, and l and out are NaN.
 __device__ __forceinline__ RowEnd end_row(const AttnArgs& a, long long at, float m2, float l, bool write) {
-  float m = l == l ? m2 * kLn2 : l, x = 1.f, y = 0.f;
+  float m = m2 * kLn2, x = 1.f, y = 0.f;
   if (a.prior_out) {
     const float pm = a.prior_m[at], pl = a.prior_l[at];
-    const float top = fmaxf(m, pm), safe = top == -INFINITY ? 0.f : top;
+    const float top = max_nan(m, pm), safe = top == -INFINITY ? 0.f : top;
     x = expf(m - safe), y = expf(pm - safe) * pl;
     l = l * x + y;
-    m = l == l ? top : l;
+    m = top;
   }
   if (write) a.m[at] = m, a.l[at] = l;
   return l == 0.f ? RowEnd{0.f, 0.f} : RowEnd{x / l * kUnbase, y == 0.f ? 0.f : y / l};   // b = 0 without a prior, l a NaN or not

@@ -35,9 +35,9 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, con
   const long long stride = (long long)gridDim.y * p.tile_rows, at = (long long)unit * p.tile_rows + blockIdx.x;
   const int cols = D / 4, groups = kThreads / cols, g = threadIdx.x / cols, d = threadIdx.x % cols * 4;
   float m = -INFINITY;
-  for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, p.ml[i * stride + at].x);
+  for (int i = threadIdx.x & 31; i < n; i += 32) m = max_nan(m, p.ml[i * stride + at].x);
 #pragma unroll
-  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+  for (int x = 16; x; x >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, x));
   const float safe = m == -INFINITY ? 0.f : m;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;

@@ -197,7 +197,7 @@ __device__ __forceinline__ void reduce_step(float (&v)[R]) {
 #pragma unroll
   for (int i = 0; i < HALF; ++i) {
     const float mine = upper ? v[HALF + i] : v[i], other = __shfl_xor_sync(~0u, upper ? v[i] : v[HALF + i], HALF);
-    v[i] = MAX ? fmaxf(mine, other) : mine + other;
+    v[i] = MAX ? max_nan(mine, other) : mine + other;
   }
   if constexpr (HALF > 1) reduce_step<HALF / 2, MAX>(v);
 }
@@ -205,7 +205,7 @@ template <bool MAX>
 __device__ __forceinline__ float reduce_rows(float (&v)[R]) {
   reduce_step<R / 2, MAX>(v);
   const float other = __shfl_xor_sync(~0u, v[0], 16);
-  return MAX ? fmaxf(v[0], other) : v[0] + other;
+  return MAX ? max_nan(v[0], other) : v[0] + other;
 }
 
 template <int FMT, int N>
@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
           bool moves = false;
           if (tid < R) {
             const float by = of_order(ex.most[tid]);
-            moves = by > (unset >> tid & 1 ? -INFINITY : kSlack);
+            // (not to +inf: the row's sums are then infinities or NaN, and its maximum stays what it is)
+            moves = by > (unset >> tid & 1 ? -INFINITY : kSlack) && by < INFINITY;
             ex.shift[tid] = moves ? by : 0.f;
             if (moves) row_r[rows0 + tid] -= by;
           }
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         for (int n = 0; n < R; ++n) {
           x[n] -= ex.shift[n];
           l[n] *= scale_of(n);
-          if (moved >> n & 1) high[n] = -INFINITY;  // all before is below this tile's largest
+          if ((moved >> n & 1) && high[n] < INFINITY) high[n] = -INFINITY;   // all before is below this tile's largest
         }
         if (i) {
 #pragma unroll 1
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
 #pragma unroll
       for (int n = 0; n < R; n += 2) {
         float2 p = make_float2(exp2_fast(x[n]), exp2_fast(x[n + 1]));
-        high[n] = fmaxf(high[n], x[n]), high[n + 1] = fmaxf(high[n + 1], x[n + 1]);
+        high[n] = max_nan(high[n], x[n]), high[n + 1] = max_nan(high[n + 1], x[n + 1]);
         const float2 sum = add2(make_float2(l[n], l[n + 1]), p);
         l[n] = sum.x, l[n + 1] = sum.y;
         // (2^kBase as part of the references would take a bit of 2^-20 from the scores)
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
         float m = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          m = fmaxf(m, ends[(wg * 4 + w) * 2 * R + tid]);
+          m = max_nan(m, ends[(wg * 4 + w) * 2 * R + tid]);
           sum += ends[(wg * 4 + w) * 2 * R + R + tid];
         }
         const float to = m == -INFINITY ? 0.f : exp2f(-m);

@@ -158,3 +158,38 @@ def test_queries_near_the_largest(fmt, D, before, bound):
     q[..., 3] = 3.4e38
     q[0, 1, 9] = -3.4e38
     strict(s, q, None, attend(s, q, None, bound), "f32")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("with_prior", [False, True])
+@pytest.mark.parametrize("io,D,before,bound", CALLS)
+def test_maxima_of_infinite_scores(fmt, with_prior, io, D, before, bound):
+    """m is the scores' maximum, +inf or NaN among them; l and out of such a row are NaN, other rows are as ever."""
+    rows, G = 6, 2
+    s = Setup(fmt, 1, D, 16, [(rows, before + rows)], seed=9)
+    t = before + rows
+    k, v = (torch.randn((t, 1, D), generator=s.gen) for _ in range(2))
+    k[..., 3] = 1.0 + torch.rand((t, 1), generator=s.gen)
+    k[..., 4] = torch.where(torch.arange(t) % 40 == 39, 1.0, -1.0)[:, None]
+    fill(s, k, v)
+    q = torch.randn((rows, G, D), generator=s.gen)
+    q[0, :, 3] = math.inf                                 # every score +inf
+    q[1, :, 3] = -math.inf                                # every score -inf
+    q[2, 1, 4] = math.inf                                 # some +inf, the others -inf
+    q[3, 0, 7] = math.nan
+    q = q.to(IO[io])
+    prior = None
+    if with_prior:
+        prior = (torch.randn((rows, G, D), generator=s.gen), torch.randn((rows, G), generator=s.gen),
+                 1 + torch.rand((rows, G), generator=s.gen))
+    got = attend(s, q, None, bound, prior=None if prior is None else tuple(x.to(DEV) for x in prior))
+    K, V = s.values()[0]
+    ro, rm, rl, _, _ = P.attend(q.double().numpy(), K, V, P.visible(rows, t, None),
+                                None if prior is None else [x.double().numpy() for x in prior])
+    out, m, l = (x.double().cpu().numpy() for x in got)
+    assert np.isposinf(rm[0]).all() and np.isposinf(rm[2, 1]) and np.isnan(rm[3, 0])
+    for test in (np.isnan, np.isposinf, np.isneginf):
+        assert np.array_equal(test(m), test(rm))
+    assert np.array_equal(np.isnan(l), np.isnan(rl)) and np.array_equal(np.isnan(out), np.isnan(ro))
+    fin = np.isfinite(rm)
+    assert np.allclose(m[fin], rm[fin], rtol=1e-3, atol=1e-3) and np.allclose(out[fin], ro[fin], rtol=2e-2, atol=2e-2)
