@@ -526,9 +526,11 @@ def _text_pair(cache: TextCache, k: torch.Tensor, v: torch.Tensor, write: bool):
             or k.shape[1:] != (cache.heads, cache.head_dim) or k.device != cache.device or v.device != cache.device):
         raise ValueError("k and v [rows, heads, head_dim] are bfloat16 or float32 tensors on the cache's GPU")
     strides = k.stride()
-    if v.stride() != strides or strides[2] != 1 or strides[0] <= 0 or strides[0] % 2 or strides[1] % 2:
+    if (v.stride() != strides or strides[2] != 1 or strides[0] <= 0 or strides[0] % 2 or strides[1] % 2
+            or (k.data_ptr() | v.data_ptr()) % (2 * k.element_size())):
         if write:
-            raise ValueError("k and v have equal even strides, and neighbouring values along head_dim")
+            raise ValueError("k and v start at an even element and have equal even strides, and neighbouring values along "
+                             "head_dim")
         k, v = (x.clone(memory_format=torch.contiguous_format) for x in (k, v))
         strides = k.stride()
     return k, v, strides
@@ -539,8 +541,9 @@ def text_append(cache: TextCache, k: torch.Tensor, v: torch.Tensor, page_table: 
                 stream: Optional[torch.cuda.Stream] = None, check: bool = False):
     """Write k, v [rows, heads, head_dim] (bfloat16 or float32) into the cache: the rows row_starts[s] ..
     row_starts[s+1] are sequence s's newest tokens, at positions kv_lens[s] - n .. kv_lens[s] - 1 (kv_lens counts
-    them).  page_table [n_seqs, max_pages], kv_lens and row_starts are int32 on the GPU.  With values, returns
-    (k, v) as the cache now holds them (rows behind the last sequence are left unset)."""
+    them).  page_table [n_seqs, max_pages], kv_lens and row_starts are int32 on the GPU.  k and v that do not start at an even
+    element, or whose strides differ or are odd, are copied first.  With values, returns (k, v) as the cache now holds
+    them (rows behind the last sequence are left unset)."""
     if _text_elsewhere(cache, stream):
         with _text_there(cache, stream):
             return text_append(cache, k, v, page_table, kv_lens, row_starts, values=values, workspace=workspace, check=check)

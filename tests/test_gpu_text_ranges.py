@@ -193,3 +193,25 @@ def test_maxima_of_infinite_scores(fmt, with_prior, io, D, before, bound):
     assert np.array_equal(np.isnan(l), np.isnan(rl)) and np.array_equal(np.isnan(out), np.isnan(ro))
     fin = np.isfinite(rm)
     assert np.allclose(m[fin], rm[fin], rtol=1e-3, atol=1e-3) and np.allclose(out[fin], ro[fin], rtol=2e-2, atol=2e-2)
+
+
+# ------------------------------------------------------------------------------------- arguments as they come ---
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_from_an_odd_element(fmt, dtype):
+    """k and v as views that start at an odd element of their storage, or have strides that differ."""
+    n, heads, D = 5, 2, 64
+    s = Setup(fmt, heads, D, 16, [(n, 20)], seed=3)
+    k, v = (torch.randn((n, heads, D), generator=s.gen).to(DEV).to(dtype) for _ in range(2))
+    want = T.text_append(s.cache, k, v, *s.batch, values=True, check=True)
+
+    def odd(x):
+        flat = torch.empty(x.numel() + 1, dtype=dtype, device=DEV)[1:]
+        return flat.view(x.shape).copy_(x)
+
+    assert odd(k).data_ptr() % (2 * k.element_size())
+    for a, b in ((odd(k), odd(v)), (k, odd(v)), (odd(k), v), (k.transpose(0, 1).contiguous().transpose(0, 1), v)):
+        got = T.text_append(s.cache, a, b, *s.batch, values=True, check=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ValueError):
+        T.text_read(s.cache, *s.batch, n_rows=n, out=(odd(k), odd(v)))
