@@ -451,9 +451,15 @@ def text_cache(fmt: str, n_pages: int, heads: int, head_dim: int, *, page_tokens
     return TextCache(fmt, *[torch.zeros((n_pages, heads, page_tokens, w), dtype=torch.uint8, device=device) for w in shapes])
 
 
+_INT_MAX = (1 << 31) - 1
+
+
 def tactkv_text_workspace_bytes(cache: TextCache, n_seqs: int, n_rows: int, q_heads: int, max_rows: int,
                                 max_kv_len: int) -> int:
-    return int(_lib.tactkv_text_workspace_bytes(cache.ptr, n_seqs, n_rows, q_heads, max_rows, max_kv_len))
+    numbers = (n_seqs, n_rows, q_heads, max_rows, max_kv_len)
+    if max(numbers) > _INT_MAX or min(numbers) < 0:   # ctypes would take them modulo 2^32
+        return 0
+    return int(_lib.tactkv_text_workspace_bytes(cache.ptr, *numbers))
 
 
 def text_workspace(cache: TextCache, *, n_seqs: int, n_rows: int, max_rows: int = 1, q_heads: int = 0,
@@ -603,6 +609,8 @@ def text_attention(q: torch.Tensor, cache: TextCache, page_table: torch.Tensor, 
     queries' attention over other tokens, as attention_decode returns it (float32).  Returns (out, m, l): out
     like q; m and l float32 [rows, q_heads], the scores' maximum and exp-sum with the prior's.  Rows behind the last
     sequence are left as they are."""
+    if not (0 <= max_rows <= _INT_MAX and (max_kv_len is None or 0 <= max_kv_len <= _INT_MAX)):
+        raise TactkvError(TACTKV_INVALID_ARG, "tactkv_text_attention")
     if _text_elsewhere(cache, stream):
         with _text_there(cache, stream):
             return text_attention(q, cache, page_table, kv_lens, row_starts, max_rows=max_rows, max_kv_len=max_kv_len,

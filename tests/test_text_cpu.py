@@ -182,3 +182,15 @@ def test_plain_grids(fmt):
     x[:, 0], x[:, 1], x[:, 2] = codes[-1], np.nextafter(mid, -np.inf), np.nextafter(mid, np.inf)
     got, _ = P.quantise(x, fmt)
     assert np.array_equal(got[:, 1], codes[:-1]) and np.array_equal(got[:, 2], codes[1:])
+
+
+def test_numbers_beyond_32_bits(T):
+    """Bounds that a C int cannot hold are refused instead of being taken modulo 2^32."""
+    c = type("Cache", (), {"ptr": cache(T)})()
+    assert T.tactkv_text_workspace_bytes(c, 1, 1, 4, 1, 64) > 0
+    for big in ((1 << 32) + 64, 1 << 32, -(1 << 32) + 64):
+        assert T.tactkv_text_workspace_bytes(c, 1, 1, 4, 1, big) == 0
+        assert T.tactkv_text_workspace_bytes(c, big, 1, 4, 1, 64) == 0
+        for kw in (dict(max_rows=1, max_kv_len=big), dict(max_rows=big, max_kv_len=64)):
+            with pytest.raises(T.TactkvError):
+                T.text_attention(None, c, None, None, None, **kw)
