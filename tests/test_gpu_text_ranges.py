@@ -31,30 +31,31 @@ CALLS = [("bf16", 64, 45, None), ("bf16", 96, 300, None), ("f32", 64, 45, None),
          ("bf16", 64, 45, 2000), ("bf16", 128, 45, 2000), ("bf16", 256, 700, None), ("bf16", 192, 250, None)]
 
 
-def strict(s, q, words, got, io, prior=None, seqs=None):
-    """got against the definition, elementwise, with the tolerance above; every finite value of it."""
-    out, m, l = (x.double().cpu().numpy() for x in got)
+def compare(fmt, D, io, got, ref, what=""):
+    """(out, m, l) of some rows against attend()'s, elementwise, with the tolerance above; every finite value of it."""
+    (out, m, l), (ro, rm, rl, A, S) = got, ref
     h_out = torch.finfo(IO[io]).eps / 2
-    h_p = 2.0 ** -24 if io == "f32" else (2.0 ** -8 if s.fmt == "bf16" else 2.0 ** -16)
+    h_p = 2.0 ** -24 if io == "f32" else (2.0 ** -8 if fmt == "bf16" else 2.0 ** -16)
+    dz = (D / 16 + 4) * 2.0 ** -23 * S
+    fin = np.isfinite(rl)
+    assert np.array_equal(np.isfinite(l), fin), what
+    assert (np.abs(m - rm)[fin] <= (dz + 2.0 ** -22 * np.abs(rm))[fin]).all(), what
+    assert (np.abs(l - rl)[fin] <= ((2 * dz + 2.0 ** -16) * rl)[fin]).all(), what
+    tol = h_out * np.abs(ro) + (h_p + 2 * dz + 2.0 ** -16)[..., None] * A + 2.0 ** -126
+    with np.errstate(invalid="ignore"):
+        bad = ~(np.abs(out - ro) <= tol) & np.isfinite(ro)
+    assert not bad.any(), (what, np.argwhere(bad)[:4], out[bad][:4], ro[bad][:4], tol[bad][:4])
+    assert np.array_equal(np.isfinite(out), np.isfinite(ro)), what
+
+
+def strict(s, q, words, got, io):
+    out, m, l = (x.double().cpu().numpy() for x in got)
     q = q.double().cpu().numpy()
     for i, ((n, t), (K, V)) in enumerate(zip(s.seqs, s.values())):
-        if seqs is not None and i not in seqs:
-            continue
         lo = s.starts()[i]
         w = None if words is None else [int(x) & (2 ** 64 - 1) for x in words[lo:lo + n]]
-        pr = None if prior is None else [x[lo:lo + n].double().cpu().numpy() for x in prior]
-        ro, rm, rl, A, S = P.attend(q[lo:lo + n], K, V, P.visible(n, t, w), pr)
         sl = slice(lo, lo + n)
-        dz = (s.D / 16 + 4) * 2.0 ** -23 * S
-        fin = np.isfinite(rl)
-        assert np.array_equal(np.isfinite(l[sl]), fin)
-        assert (np.abs(m[sl] - rm)[fin] <= (dz + 2.0 ** -22 * np.abs(rm))[fin]).all()
-        assert (np.abs(l[sl] - rl)[fin] <= ((2 * dz + 2.0 ** -16) * rl)[fin]).all()
-        tol = h_out * np.abs(ro) + (h_p + 2 * dz + 2.0 ** -16)[..., None] * A + 2.0 ** -126
-        with np.errstate(invalid="ignore"):
-            bad = ~(np.abs(out[sl] - ro) <= tol) & np.isfinite(ro)
-        assert not bad.any(), (i, np.argwhere(bad)[:4], out[sl][bad][:4], ro[bad][:4], tol[bad][:4])
-        assert np.array_equal(np.isfinite(out[sl]), np.isfinite(ro))
+        compare(s.fmt, s.D, io, (out[sl], m[sl], l[sl]), P.attend(q[sl], K, V, P.visible(n, t, w)), i)
 
 
 def fill(s, k, v):
@@ -193,6 +194,77 @@ def test_maxima_of_infinite_scores(fmt, with_prior, io, D, before, bound):
     assert np.array_equal(np.isnan(l), np.isnan(rl)) and np.array_equal(np.isnan(out), np.isnan(ro))
     fin = np.isfinite(rm)
     assert np.allclose(m[fin], rm[fin], rtol=1e-3, atol=1e-3) and np.allclose(out[fin], ro[fin], rtol=2e-2, atol=2e-2)
+
+
+# ------------------------------------------------------------------------------------ many tiles in one block ---
+class Crowd:
+    """160 sequences over one K/V head that read the same pages, so many that none is split and a block walks through all
+    of its tokens, 128 at a time; their lengths differ."""
+
+    def __init__(self, fmt, D, rows, G, T_max, page=64, seed=1):
+        self.s = s = Setup(fmt, 1, D, page, [(rows, T_max)], seed=seed)
+        self.rows, self.G, self.n, self.T = rows, G, 160, T_max
+        self.lens = [T_max - 61 * (i % 9) for i in range(self.n)]
+        self.starts = ints([rows * i for i in range(self.n + 1)])
+        self.k, self.v = (torch.randn((T_max, 1, D), generator=s.gen) for _ in range(2))
+        self.q = torch.randn((rows * self.n, G, D), generator=s.gen).bfloat16()
+
+    def run(self, words=None, bad_pages=()):
+        """Attention of every sequence; three of each length's are checked, with bad_pages' tokens unseen."""
+        s, rows = self.s, self.rows
+        fill(s, self.k, self.v)
+        table = s.batch[0].repeat(self.n, 1)
+        for i, page in enumerate(bad_pages):
+            table[:, page] = (-1, s.cache.n_pages, 1 << 30, -(1 << 31))[i % 4]
+        ws = T.text_workspace(s.cache, n_seqs=self.n, n_rows=rows * self.n, max_rows=rows, q_heads=self.G, max_kv_len=self.T)
+        tree = None if words is None else torch.tensor(words * self.n, dtype=torch.int64, device=DEV)
+        got = T.text_attention(self.q.to(DEV), s.cache, table, ints(self.lens), self.starts, max_rows=rows, max_kv_len=self.T,
+                               tree=tree, workspace=ws)
+        status = T.tactkv_device_status(ws.data_ptr(), ws.numel(), 0)
+        assert status == (T.TACTKV_INVALID_ARG if bad_pages else T.TACTKV_OK)
+        out, m, l = (x.double().cpu().numpy() for x in got)
+        K, V = s.values()[0]
+        for i in list(range(9)) + [77, self.n - 1]:
+            t, sl = self.lens[i], slice(rows * i, rows * (i + 1))
+            seen = P.visible(rows, t, None if words is None else [w & (2 ** 64 - 1) for w in words])
+            for page in bad_pages:
+                seen[:, page * s.page:(page + 1) * s.page] = False
+            ref = P.attend(self.q[sl].double().numpy(), K[:, :t], V[:, :t], seen)
+            compare(s.fmt, s.D, "bf16", (out[sl], m[sl], l[sl]), ref, i)
+
+
+# (head_dim, rows, query heads to a K/V head): units of 16, 32 and 64 rows; the first on the other kernel
+CROWDS = [(96, 4, 4), (64, 2, 5), (64, 8, 8), (128, 4, 4), (128, 3, 8), (128, 7, 8), (192, 4, 4), (192, 5, 6), (256, 1, 16), (256, 5, 4)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,rows,G", CROWDS)
+@pytest.mark.parametrize("kind", ["grow", "shrink", "climb"])
+def test_values_and_scores_that_change_from_tile_to_tile(fmt, D, rows, G, kind):
+    """V that grows or shrinks by 2^9 with each tile; scores that rise, so that the references move in most tiles."""
+    c = Crowd(fmt, D, rows, G, 1500)
+    tile = torch.arange(1500) // 128
+    if kind == "climb":
+        c.q[..., 0] = 4.0
+        c.k[:, 0, 0] = torch.arange(1500) * (20.0 / 1500) * math.sqrt(D)      # scores from 0 to 80
+    else:
+        c.v *= torch.ldexp(torch.ones(1500), (9 if kind == "grow" else -9) * tile)[:, None, None]
+    c.run()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,rows,G", CROWDS)
+@pytest.mark.parametrize("drafts", ["plain", "odd"])
+def test_bad_pages_in_many_tiles(fmt, D, rows, G, drafts):
+    """Pages out of range in tiles 0, 3, 17 and the last one; drafted tokens, each its own row's alone, with infinities and
+    NaN in their V."""
+    c = Crowd(fmt, D, rows, G, 2650 + rows)
+    words = [1 << j for j in range(rows)]
+    if drafts == "odd":
+        c.lens = [c.T] * c.n                              # (a shorter sequence's drafts would be a longer one's past)
+        c.v[c.T - 1, 0, 33] = math.inf
+        c.v[c.T - rows, 0, 5] = math.nan
+    c.run(words, bad_pages=(0, 7, 34, 40))
 
 
 # ------------------------------------------------------------------------------------- arguments as they come ---
