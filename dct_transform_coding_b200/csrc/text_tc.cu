@@ -50,7 +50,13 @@ constexpr int kMaxSlots = 12;
 constexpr int R = 16;                             // rows of a softmax warpgroup
 constexpr float kToLog2 = to_log2(D);
 constexpr uint32_t kPolls = 1u << 16;             // of a wait; each suspends the thread for up to kPause ns
+// A test's build polls without suspending, and less often where a wait may give up (those with `dead`).
+#ifdef TACTKV_TEXT_POLLS
+constexpr uint32_t kPause = 0;
+#else
+#define TACTKV_TEXT_POLLS kPolls
 constexpr uint32_t kPause = 20000;
+#endif
 
 template <int FMT, int N>
 struct Shape {
@@ -119,14 +125,20 @@ static_assert(sizeof(Exchange) == 144, "");
 // SLEEP: for waits with time to spare, whose polls would take issue slots from the warps that work.
 template <bool SLEEP = false>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  const uint32_t a = tc::smem_u32(bar);
-  for (uint32_t i = 0; i < kPolls; ++i) {
+  const uint32_t a = tc::smem_u32(bar), polls = dead ? TACTKV_TEXT_POLLS : kPolls;
+  for (uint32_t i = 0; i < polls; ++i) {
     uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(a), "r"(parity), "r"(kPause)
-        : "memory");
+    if constexpr (kPause > 0)
+      asm volatile(
+          "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(done)
+          : "r"(a), "r"(parity), "r"(kPause)
+          : "memory");
+    else
+      asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                   : "=r"(done)
+                   : "r"(a), "r"(parity)
+                   : "memory");
     if (done) return true;
     if (dead && (i & 15) == 15 && *dead) return false;
     if constexpr (SLEEP) __nanosleep(50);
@@ -264,7 +276,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   const int my_half = lane / of_part, my_place = lane % of_part * run;
   const uint32_t of_half = (2u << (of_part - 1)) - 1;
   bool copies_ok = true;
-  int last_copy[2] = {-1, -1};                     // of K's and V's tiles
+  int last_copy[2][Sh::kParts];                    // of K's and V's tiles, in each part's slots
+  for (int half = 0; half < Sh::kParts; ++half) last_copy[0][half] = last_copy[1][half] = -1;
   long long at = 0, at_next = 0;                   // the lane's run of this V's and the next K's tile
   uint32_t good = 0, good_next = 0;                // the lanes whose runs are there
   int page_ahead = -1;                             // of the lane's run in the tile after
@@ -299,7 +312,8 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (lane < kAtOnce)
         tc::mbar_expect_tx(&bars->slot_full[slot_of(i, kv, first + lane)],
                            __popc(mask >> ((first + lane) * of_part) & of_half) * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
-      last_copy[kv] = i;
+#pragma unroll
+      for (int half = first; half < first + kAtOnce; ++half) last_copy[kv][half] = i;
       __syncwarp();
       if ((mask >> lane & 1) && my_half >= first && my_half < first + kAtOnce) {
         const int slot = slot_of(i, kv, my_half);
@@ -398,11 +412,14 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (copies_ok && !(kCoded && i == 0)) copy(1, i);
     }
     // No copy is in flight when the block ends, not even one whose readers gave up.
-    for (int kv = 0; kv < 2; ++kv) {
-      const int newest = kCoded ? last_copy[kv] : max(turn_of(last_copy[0], 0), last_copy[1] < 0 ? 0 : turn_of(last_copy[1], 1));
-      for (int i = last_copy[kv]; i >= 0 && turn_of(i, kv) + kRing > newest; --i)
-        for (int half = 0; half < Sh::kParts; ++half) wait<true>(&bars->slot_full[slot_of(i, kv, half)], round_of(i, kv) & 1, nullptr);
-    }
+    // (A part's own last copy: asked for a phase that its barrier has not reached, the one before's end would pass for it.)
+    const int newest = kCoded ? 0 : max(turn_of(last_copy[0][0], 0), last_copy[1][0] < 0 ? 0 : turn_of(last_copy[1][0], 1));
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int half = 0; half < Sh::kParts; ++half)
+        for (int i = last_copy[kv][half]; i >= 0 && turn_of(i, kv) + kRing > (kCoded ? last_copy[kv][half] : newest); --i)
+          wait<true>(&bars->slot_full[slot_of(i, kv, half)], round_of(i, kv) & 1, nullptr);
   } else if (warp == kIssuer) {
     // -------------------------------------------------------------------------------- issuer ---
     // The whole warp goes along, so that descriptors stay in uniform registers; one lane issues.
