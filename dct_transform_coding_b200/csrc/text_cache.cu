@@ -174,9 +174,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Cache c, const B
           w[0] = s == 255u ? 0u : pack_e4m3x4(x[0], x[1], x[2], x[3]);
           w[1] = s == 255u ? 0u : pack_e4m3x4(x[4], x[5], x[6], x[7]);
         } else {
-          // The shuffle (of a lane's own word) keeps the compiler from folding the unpacking of the values
-          // below into this packing: nvcc 12.9 then loses the word's upper bytes.
-          w[0] = __shfl_sync(~0u, s == 255u ? 0u : pack_e2m1x8(x), threadIdx.x & 31);
+          w[0] = s == 255u ? 0u : pack_e2m1x8(x);
         }
         if (mine && (threadIdx.x & 3) == 0) c.scales[kv][at * (c.head_dim / kGroup) + d / kGroup] = (unsigned char)s;
       }
@@ -185,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Cache c, const B
         void* out = kv ? v_values : k_values;
         if (out) {
           float y[8];
-          decode8<FMT>(w, s, y);
+          decode8<FMT, true>(w, s, y);
           store8<F32, true>(out, (long long)row * width + e, y);
         }
       }
