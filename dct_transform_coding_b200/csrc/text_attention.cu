@@ -527,7 +527,7 @@ template <int FMT, bool F32>
 cudaError_t launch(const AttnArgs& a, const Parts& p, cudaStream_t st) {
   if (p.tile_rows == 8) return launch<FMT, F32, 1>(a, p, st);
   if (p.tile_rows == 16) return launch<FMT, F32, 2>(a, p, st);
-  if constexpr (D <= kWideDim && FMT == kBf16) return launch<FMT, F32, 4>(a, p, st);
+  if constexpr (wide_tiles(FMT, F32, D)) return launch<FMT, F32, 4>(a, p, st);
   return cudaErrorInvalidValue;
 }
 

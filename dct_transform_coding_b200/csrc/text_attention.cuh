@@ -21,6 +21,13 @@ constexpr int kWideDim = 128;      // up to this head_dim a unit may have twice 
 
 constexpr int kPartRows(int D) { return D <= kWideDim ? 64 : 32; }
 
+// Whether text_attention.cu has tiles of 32 rows.  16 sequences x 4 heads x 6000 tokens, 32 rows in two tiles of 16 against
+// one of 32: float32 queries, head_dim 128 148 against 111 us (bfloat16 cache), 140 against 97 (8 bits); bfloat16 queries on
+// coded caches, head_dim 32 42 against 28, but 96 75 against 79 (4 bits), and 128 rows 133 against 142.
+__host__ __device__ constexpr bool wide_tiles(int fmt, bool f32, int D) {
+  return D <= kWideDim && (f32 || fmt == kBf16 || D == 32);
+}
+
 // Up to one tile of text_tc.cu's the kernel of text_attention.cu is used: its start is shorter (100 tokens, 4 heads x 128, 8
 // bits: 7.3 against 8.7 us, bfloat16 6.8 against 7.1).  At 256 tokens 8 bits take 9.6 and 9.5, bfloat16 9.3 and 7.6,
 // and with more rows or tokens it falls behind (32 sequences x 8 heads x 6001 tokens, 24 rows, 4 bits: 199 against 103).

@@ -82,10 +82,9 @@ cudaError_t launch_attention(int fmt, bool f32, const AttnArgs& a, void* workspa
 #undef TACTKV_CASE
     }
   } else {
-    // 16 sequences x 4 heads x 128 x 6000 tokens, float32 queries: 4 rows take 66 us in tiles of 8, 79 of 16 and 106 of 32;
-    // 12 rows 114 in two of 8, 80 in one of 16.  32 rows take 149 us in two tiles of 16 and 110 in one of 32 with a bfloat16
-    // cache; coded ones have more to keep in registers: 77 in either, and 128 rows 228 in tiles of 16 and 248 of 32.
-    plan(a, rows <= 8 ? 8 : (rows <= 16 || D > kWideDim || fmt != kBf16 ? 16 : 32), kMaxParts, kShortPart, p);
+    // 16 sequences x 4 heads x 128 x 6000 tokens, float32 queries: 4 rows take 66 us in tiles of 8, 79 of 16 and 106 of 32
+    // (8 bits: 42, 73, 92); 12 rows 115 in two of 8, 79 in one of 16 (8 bits: 75, 74).
+    plan(a, rows <= 8 ? 8 : (rows <= 16 || !wide_tiles(fmt, f32, D) ? 16 : 32), kMaxParts, kShortPart, p);
     switch (D) {
 #define TACTKV_CASE(D) case D: e = launch_parts_##D(fmt, f32, a, p, st); break;
       TACTKV_FOR_D(TACTKV_CASE)
