@@ -276,8 +276,10 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
   const int my_half = lane / of_part, my_place = lane % of_part * run;
   const uint32_t of_half = (2u << (of_part - 1)) - 1;
   bool copies_ok = true;
-  int last_copy[2][Sh::kParts];                    // of K's and V's tiles, in each part's slots
-  for (int half = 0; half < Sh::kParts; ++half) last_copy[0][half] = last_copy[1][half] = -1;
+  constexpr int kAtOnce = kRing > 1 ? Sh::kParts : 1;   // a tile's parts copied together (a lone slot's copy does not wait for the other's)
+  int last_copy[2][Sh::kParts / kAtOnce];          // of K's and V's tiles
+#pragma unroll
+  for (int x = 0; x < Sh::kParts / kAtOnce; ++x) last_copy[0][x] = last_copy[1][x] = -1;
   long long at = 0, at_next = 0;                   // the lane's run of this V's and the next K's tile
   uint32_t good = 0, good_next = 0;                // the lanes whose runs are there
   int page_ahead = -1;                             // of the lane's run in the tile after
@@ -303,7 +305,6 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     const long long from = kv ? at : at_next;
     const uint32_t mask = kv ? good : good_next;
     const int round = round_of(i, kv);
-    constexpr int kAtOnce = kRing > 1 ? Sh::kParts : 1;   // (a lone slot's copy does not wait for the other half's)
 #pragma unroll
     for (int first = 0; first < Sh::kParts; first += kAtOnce) {
       if (round) copies_ok = wait(&bars->slot_free[slot_of(i, kv, first + lane % kAtOnce)], (round - 1) & 1, dead);
@@ -312,8 +313,7 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
       if (lane < kAtOnce)
         tc::mbar_expect_tx(&bars->slot_full[slot_of(i, kv, first + lane)],
                            __popc(mask >> ((first + lane) * of_part) & of_half) * run * (Sh::kRow + (kCoded ? D / kGroup : 0)));
-#pragma unroll
-      for (int half = first; half < first + kAtOnce; ++half) last_copy[kv][half] = i;
+      last_copy[kv][first / kAtOnce] = i;
       __syncwarp();
       if ((mask >> lane & 1) && my_half >= first && my_half < first + kAtOnce) {
         const int slot = slot_of(i, kv, my_half);
@@ -413,13 +413,15 @@ __global__ void __launch_bounds__(Shape<FMT, N>::kThreads, Shape<FMT, N>::kCtas)
     }
     // No copy is in flight when the block ends, not even one whose readers gave up.
     // (A part's own last copy: asked for a phase that its barrier has not reached, the one before's end would pass for it.)
-    const int newest = kCoded ? 0 : max(turn_of(last_copy[0][0], 0), last_copy[1][0] < 0 ? 0 : turn_of(last_copy[1][0], 1));
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-      for (int half = 0; half < Sh::kParts; ++half)
-        for (int i = last_copy[kv][half]; i >= 0 && turn_of(i, kv) + kRing > (kCoded ? last_copy[kv][half] : newest); --i)
-          wait<true>(&bars->slot_full[slot_of(i, kv, half)], round_of(i, kv) & 1, nullptr);
+    for (int x = 0; x < Sh::kParts / kAtOnce; ++x)
+      for (int kv = 0; kv < 2; ++kv) {
+        const int last = last_copy[kv][x];
+        const int newest = kCoded ? last : max(turn_of(last_copy[0][x], 0), last_copy[1][x] < 0 ? 0 : turn_of(last_copy[1][x], 1));
+        for (int i = last; i >= 0 && turn_of(i, kv) + kRing > newest; --i)
+          for (int half = x * kAtOnce; half < (x + 1) * kAtOnce; ++half)
+            wait<true>(&bars->slot_full[slot_of(i, kv, half)], round_of(i, kv) & 1, nullptr);
+      }
   } else if (warp == kIssuer) {
     // -------------------------------------------------------------------------------- issuer ---
     // The whole warp goes along, so that descriptors stay in uniform registers; one lane issues.

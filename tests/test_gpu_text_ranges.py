@@ -39,7 +39,9 @@ def compare(fmt, D, io, got, ref, what=""):
     dz = (D / 16 + 4) * 2.0 ** -23 * S
     fin = np.isfinite(rl)
     assert np.array_equal(np.isfinite(l), fin), what
-    assert (np.abs(m - rm)[fin] <= (dz + 2.0 ** -22 * np.abs(rm))[fin]).all(), what
+    assert np.array_equal(np.isneginf(m), np.isneginf(rm)), what
+    some = np.isfinite(rm)
+    assert (np.abs(m[some] - rm[some]) <= dz[some] + 2.0 ** -22 * np.abs(rm[some])).all(), what
     assert (np.abs(l - rl)[fin] <= ((2 * dz + 2.0 ** -16) * rl)[fin]).all(), what
     tol = h_out * np.abs(ro) + (h_p + 2 * dz + 2.0 ** -16)[..., None] * A + 2.0 ** -126
     with np.errstate(invalid="ignore"):
