@@ -114,17 +114,6 @@ __device__ __forceinline__ void unpack_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
-// The same by integer operations and one multiplication a pair: a code's magnitude bits are those of a half-precision value
-// 2^-14 as large.
-__device__ __forceinline__ void widen_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = w >> (8 * i), pair = (u & 0xFu) | (u & 0xF0u) << 12;
-    const uint32_t b = (pair & 0x00080008u) << 12 | (pair & 0x00070007u) << 9;
-    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&b), __float2half2_rn(16384.f));
-    h[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
 // Two E4M3 codes (16 bits) as float32.
 __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
@@ -138,14 +127,12 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 
-// Eight neighbouring values of one token and head from their codes (16, 8 or 4 bytes in w[]).  PACKED: from a word
-// that this thread has just packed, of which unpack_e2m1x8() as nvcc 12.9 compiles it gave the lowest byte's values alone.
-template <int FMT, bool PACKED = false>
+// Eight neighbouring values of one token and head from their codes (16, 8 or 4 bytes in w[]).
+template <int FMT>
 __device__ __forceinline__ void decode8(const uint32_t (&w)[4], uint32_t scale, float (&x)[8]) {
   const float f = FMT == kBf16 ? 1.f : scale_value(scale);
   uint32_t h[4];
-  if constexpr (FMT == kFp4 && PACKED) widen_e2m1x8(w[0], h);
-  else if constexpr (FMT == kFp4) unpack_e2m1x8(w[0], h);
+  if constexpr (FMT == kFp4) unpack_e2m1x8(w[0], h);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 v;
