@@ -14,12 +14,13 @@
 //
 // What bounds it: instructions (decoding, splitting into terms, the softmax, for 16 tokens and 8 rows at a time), and
 // the latency of a warp's steps where there are few.  16 sequences x 4 heads x 128 x 3000 to 6000 tokens, 4 rows, float32
-// queries: bfloat16 cache 66 us, 2.2 TB/s; 8 bits 35 us, 2.1 TB/s; one tile of 100 tokens 7 us.
+// queries: bfloat16 cache 66 us, 2.2 TB/s; 8 bits 42 us, 1.8 TB/s; one tile of 100 tokens 8 us.
 //
-// A coded value, code * 2^e, is a bfloat16 exactly (what float32 holds below 2^-126 aside), and so it goes into the products:
+// A coded value, code * 2^e, is a bfloat16 exactly (what bfloat16 drops below 2^-126 aside), and so it goes into the products:
 // no value needs another's scale, and magnitudes may differ by all that bfloat16 holds, within a token and between tokens,
-// seen or not.  (Half precision relative to the largest scale so far was a product fewer for P and a third fewer for float32
-// queries, but a large V in a token that a row does not see took that row's probabilities below half precision's range.)
+// seen or not.  (Half precision relative to the largest scale so far took a product fewer for P and fewer terms for float32
+// queries: 35 us for the 42 above, 30 for 36 at head_dim 96.  But a large V in a token that a row does not see took that row's
+// probabilities below half precision's range.)
 // Queries: bfloat16 ones go in as they are, float32 ones as three bfloat16 terms.  The probabilities are one term for bfloat16
 // caches, two for coded ones, whose values have 4 bits or 2 themselves, and three for float32 queries.
 #include <atomic>

@@ -29,8 +29,8 @@ __host__ __device__ constexpr bool wide_tiles(int fmt, bool f32, int D) {
 }
 
 // Up to one tile of text_tc.cu's the kernel of text_attention.cu is used: its start is shorter (100 tokens, 4 heads x 128, 8
-// bits: 7.3 against 8.7 us, bfloat16 6.8 against 7.1).  At 256 tokens 8 bits take 9.6 and 9.5, bfloat16 9.3 and 7.6,
-// and with more rows or tokens it falls behind (32 sequences x 8 heads x 6001 tokens, 24 rows, 4 bits: 199 against 103).
+// bits: 7.8 against 9.6 us, bfloat16 6.8 against 7.6).  At 256 tokens 8 bits take 10.0 and 9.9, bfloat16 9.2 and 8.2,
+// and with more rows or tokens it falls behind (32 sequences x 8 heads x 6001 tokens, 24 rows, 4 bits: 269 against 116).
 constexpr int kOneTile = 128;
 
 // A unit is (sequence, K/V head, tile of tile_rows rows), numbered in that order.
@@ -145,10 +145,10 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 // The split of a launch into at most `blocks` blocks, and each sequence into parts, which have at least kLeastPart tokens:
-// with half of that the sum over more parts costs more than it gains (4000 tokens x 4 heads x 128, tcgen05: bfloat16 11.8
-// against 11.2 us, 8 bits 13.5 against 12.6; head_dim 96 on the other kernel: 17.7 against 13.7).  kShortPart is used where
-// it makes few parts (kFewParts) and no SM gets two: 1000 tokens 9.1 against 9.5 us, 8 bits 11.0 against 11.6
-// and, on the other kernel, 9.7 against 11.8 and 17.3 against 22.8 (float32, head_dim 256).  Sequences
+// with half of that the sum over more parts costs more than it gains (4000 tokens x 4 heads x 128, tcgen05: bfloat16 12.3
+// against 11.7 us, 8 bits 14.0 against 13.5; on the other kernel, head_dim 96, it gains: 12.3 against 14.4).  kShortPart is
+// used where it makes few parts (kFewParts) and no SM gets two: 1000 tokens 9.5 against 10.1 us, 8 bits 12.0 against 12.6
+// and, on the other kernel, 10.4 against 13.2 (head_dim 96) and 16.3 against 24.5 (float32, head_dim 256, 700 tokens).  Sequences
 // of up to `whole` tokens are not split.
 inline void plan(const AttnArgs& a, int tile_rows, int blocks, int whole, Parts& p) {
   p.tile_rows = tile_rows;

@@ -14,21 +14,21 @@
 // Every wait is bounded; one that expires records TACTKV_TIMEOUT and ends the block's work.
 //
 // The running maximum is lazy: a reference that scores may pass by kSlack before it, the sums and O move, so that O stays in
-// tensor memory (moved with every higher score: 237 against 173 us, 4 sequences x 8 heads x 504 rows, 8111 tokens).
+// tensor memory (moved with every higher score: 276 against 189 us, 4 sequences x 8 heads x 504 rows, 8111 tokens).
 // Coded caches: a value, code * 2^e, is a bfloat16 exactly, so no value needs another's scale.  (In half precision relative
 // to the largest scale so far, a large V that a row does not see took the row's probabilities below that type's range.)
-// P is bfloat16: one term for bfloat16 caches, so rounded to 8 bits, two terms, 16 bits, for coded ones, whose products with
-// P's second term take no time that the decoders do not.  l is summed in float32 before the rounding.
+// P is bfloat16: two terms, 16 bits, for coded caches, but one, 8 bits, for bfloat16 ones, where a second would bring bfloat16
+// outputs from 2.1e-3 of the exact ones to 1.7e-3 and cost 17 % at 64 rows (112 to 130 us, 4 sequences x 8 heads x 504 rows)
+// and 1 to 6 % below.  l is summed in float32 before the rounding.
 //
-// What bounds it.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, 4000 to 8000 tokens, 16 rows: 121 to 127 us, 6.2 TB/s).
-// Coded ones: the roles' own chains of latencies (the same sizes: 131 us at 8 bits, 126 at 4, so 3.1 and 1.7 TB/s).  By
-// clock readings in each role a tile of K costs its decoders about 2600 cycles, half of them waits and hand-overs, and
-// with 64 rows a tile costs the softmax about 3300.  A block's start and end cost 7 to 12 us.
+// What bounds it.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, 4000 to 8000 tokens, 16 rows: 122 to 124 us, 6.2 TB/s).
+// Coded ones: the roles' own chains of latencies (the same sizes: 139 us at 8 bits and at 4, so 2.9 and 1.5 TB/s).  By
+// clock readings in each role a tile costs K's decoders 2500 cycles with 16 rows and 3200 with 64, a third of them waits, and
+// the softmax 1400 and 2900.  A block's start and end cost 7 to 12 us.
 //
 // An infinity or NaN in the V of a drafted token must reach only the rows that see it, so it is taken out of
 // the operand, and its rows get it in plain arithmetic at the end.
 #include <atomic>
-#include <cfloat>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -76,17 +76,17 @@ struct Shape {
   // With an odd number of blocks the last product reads a block past V's operand: something must be there.
   static constexpr int kPad = kBlocks % 2 ? kBlock : 0;
   static constexpr int kFixed = kQ + kMisc + kPad;
-  // Two blocks on an SM: one's start, end and waits are the other's time.  bfloat16: 21.2 against 23.7 us where a launch is
-  // split into one wave (16 sequences x 4 heads x 128 x 4090 tokens, 7 rows), 127 against 120 in several (64 sequences x
-  // 8000).  Coded, 64 sequences x 4 heads x 8000 tokens, 16 rows: head_dim 64 98 against 121 us; but 128, 4 bits: 136
-  // against 126.
+  // Two blocks on an SM: one's start, end and waits are the other's time.  bfloat16: 20.9 against 22.8 us where a launch is
+  // split into one wave (16 sequences x 4 heads x 128 x 4090 tokens, 7 rows), 122 against 120 in several (64 sequences x
+  // 8000).  Coded, 64 sequences x 4 heads x 8000 tokens, 16 rows: head_dim 64 98 against 134 us; 128 fits at 4 bits alone,
+  // 127 against 139, but 15.4 against 13.5 for one sequence of 4000 tokens.
   static constexpr int kLeast = kFixed + 2 * kP + (kCoded ? 2 * kOp : 0) + 2 * kParts * kSlot;   // bytes, with two slots each
   static constexpr int kCtas = N <= (kCoded ? 16 : 32) && (!kCoded || D == 64) && kLeast <= 113 * 1024 ? 2 : 1;
-  // V operands in turn: two where they leave the raw slots enough (32 sequences x 8 heads, 24 rows: 103 against 109 us)
+  // V operands in turn: two where they leave the raw slots enough (32 sequences x 8 heads, 24 rows: 117 against 123 us)
   static constexpr int kVOps = kCoded && kCtas == 1 && D <= 128 ? 2 : 1;
   static constexpr int kOps = kCoded ? (1 + kVOps) * kOp : 0;
-  // head_dim 256, 32 sequences x 4 heads x 8000 tokens: 142 us with 16 warps, 160 with 8; 128, 24 rows: 118 with 16, 114
-  // with 8; 192, of whose three blocks of 64 columns a lane always takes the same one if groups have three warps: 150 with
+  // head_dim 256, 32 sequences x 4 heads x 8000 tokens: 150 us with 16 warps, 183 with 8; 128, 64 sequences: 148 with 16, 143
+  // with 8; 192, of whose three blocks of 64 columns a lane always takes the same one if groups have three warps: 140 with
   // 12, 179 with 16
   static constexpr int kDecoders = !kCoded ? 0 : (D == 192 ? 12 : (D > 128 ? 16 : 8));
   static constexpr int kThreads = 32 * (4 * kWGs + 2 + kDecoders);
@@ -866,14 +866,14 @@ cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
   }
   CUtensorMap maps[2] = {};
   if (FMT == kBf16 && !(make_map(a, 0, &maps[0]) && make_map(a, 1, &maps[1]))) return cudaErrorInvalidValue;
-  plan(a, N, kSms * Sh::kCtas, 2 * TT, p);   // (two tiles: 7.6 us whole, 8.5 in parts)
+  plan(a, N, kSms * Sh::kCtas, 2 * TT, p);   // (two tiles: 8.3 us whole, 8.8 in parts)
   tc_kernel<FMT, N><<<dim3(p.count, a.c.heads * p.tiles, a.b.n_seqs), Sh::kThreads, Sh::kSmem, st>>>(a, p, maps[0], maps[1]);
   return cudaGetLastError();
 }
 template <int FMT>
 cudaError_t launch(const AttnArgs& a, Parts& p, cudaStream_t st) {
-  // The narrowest tile that takes all rows (64 sequences x 4 heads x 8000 tokens, 8 bits): 16 rows in 64 columns take 167
-  // us, in 16 columns 131; 64 rows in two tiles of 32, which decode K and V twice, 272, in one 176.
+  // The narrowest tile that takes all rows (64 sequences x 4 heads x 8000 tokens, 8 bits): 16 rows in 64 columns take 183
+  // us, in 16 columns 143; 64 rows in two tiles of 32, which decode K and V twice, 297, in one 185.
   const int rows = a.max_rows * (a.q_heads / a.c.heads);
   if (rows <= 16) return launch<FMT, 16>(a, p, st);
   if (rows <= 32 || D > kWideDim) return launch<FMT, 32>(a, p, st);

@@ -317,8 +317,12 @@ tactkv_status tactkv_text_read(const tactkv_text_cache* cache, const tactkv_text
                  over the tokens seen (and the prior's), 16-byte aligned;
      m, l        float32 [n_rows][q_heads]: the scores' maximum and sum_t exp(score - m).
    A row that sees nothing gets out = 0, m = -inf, l = 0.  Values at positions that a row does not see
-   do not reach it, be they infinities or NaN.  Scores and sums are float32; with bfloat16 q the
-   probabilities are rounded to 11 or 8 bits before they multiply V, with float32 q they are not.
+   do not reach it, however large, infinities and NaN among them.  A row with a score of +inf or NaN has that
+   as m, and NaN as l and in out.  K and V enter the products as the values that the codes stand for, in
+   bfloat16's range.  Scores and sums are float32.  Before they multiply V the probabilities are rounded to 8
+   bits (TACTKV_TEXT_BF16) or 16 (the coded formats) with bfloat16 q, to 24 with float32 q; the sums are of
+   2^-16 times their products with V, so that V may come near bfloat16's largest value, and products with |V|
+   below 2^-102 lose bits.
    No output may overlap an input or another output.  workspace: tactkv_text_workspace_bytes() with the same
    numbers, 256-byte aligned; calls that may overlap in time need workspaces of their own.  Asynchronous on
    `stream`; one kernel, or two where sequences are split. */
