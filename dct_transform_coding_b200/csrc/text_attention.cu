@@ -14,7 +14,7 @@
 //
 // What bounds it: instructions (decoding, splitting into terms, the softmax, for 16 tokens and 8 rows at a time), and
 // the latency of a warp's steps where there are few.  16 sequences x 4 heads x 128 x 3000 to 6000 tokens, 4 rows, float32
-// queries: bfloat16 cache 66 us, 2.2 TB/s; 8 bits 42 us, 1.8 TB/s; one tile of 100 tokens 8 us.
+// queries: bfloat16 cache 66 us, 2.3 TB/s; 8 bits 42 us, 1.8 TB/s; one tile of 100 tokens 8 us.
 //
 // A coded value, code * 2^e, is a bfloat16 exactly (what bfloat16 drops below 2^-126 aside), and so it goes into the products:
 // no value needs another's scale, and magnitudes may differ by all that bfloat16 holds, within a token and between tokens,

@@ -21,7 +21,7 @@
 // outputs from 2.1e-3 of the exact ones to 1.7e-3 and cost 17 % at 64 rows (112 to 130 us, 4 sequences x 8 heads x 504 rows)
 // and 1 to 6 % below.  l is summed in float32 before the rounding.
 //
-// What bounds it.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, 4000 to 8000 tokens, 16 rows: 122 to 124 us, 6.2 TB/s).
+// What bounds it.  bfloat16 caches: HBM (64 sequences x 4 heads x 128, 4000 to 8000 tokens, 16 rows: 122 to 124 us, 6.4 TB/s).
 // Coded ones: the roles' own chains of latencies (the same sizes: 139 us at 8 bits and at 4, so 2.9 and 1.5 TB/s).  By
 // clock readings in each role a tile costs K's decoders 2500 cycles with 16 rows and 3200 with 64, a third of them waits, and
 // the softmax 1400 and 2900.  A block's start and end cost 7 to 12 us.

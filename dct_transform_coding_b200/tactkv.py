@@ -608,7 +608,8 @@ def text_attention(q: torch.Tensor, cache: TextCache, page_table: torch.Tensor, 
     max_kv_len bounds kv_lens (default: what the page table holds).  prior = (out, m, l) merges the same
     queries' attention over other tokens, as attention_decode returns it (float32).  Returns (out, m, l): out
     like q; m and l float32 [rows, q_heads], the scores' maximum and exp-sum with the prior's.  Rows behind the last
-    sequence are left as they are."""
+    sequence are left as they are.  Without workspace (text_workspace) the call makes and zeroes its own, of 5 to 20 MB; what the
+    kernels find wrong is in the workspace, and raised with check."""
     if not (0 <= max_rows <= _INT_MAX and (max_kv_len is None or 0 <= max_kv_len <= _INT_MAX)):
         raise TactkvError(TACTKV_INVALID_ARG, "tactkv_text_attention")
     if _text_elsewhere(cache, stream):
